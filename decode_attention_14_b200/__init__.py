@@ -33,6 +33,9 @@ RQ_ERR_TIMEOUT = -7
 RQ_FMT_RESIDUAL = 0
 RQ_FMT_BF16 = 1
 
+RQ_OUT_FP32 = 0
+RQ_OUT_BF16 = 1
+
 HEAD_DIM = 128
 
 
@@ -104,6 +107,9 @@ def _load() -> ctypes.CDLL:
     L.rq_cache_length_seq.argtypes = [vp, i32, i32, i32, ctypes.POINTER(i32)]
     L.rq_cache_export.restype = i32
     L.rq_cache_export.argtypes = [vp, i32, i32, vp, vp, vp, vp]
+    i64 = ctypes.c_int64
+    L.rq_cache_read.restype = i32
+    L.rq_cache_read.argtypes = [vp, i32, i32, i32, i32, i32, vp, vp, i64, i64, i64, vp]
     L.rq_decode_bytes.restype = ctypes.c_size_t
     L.rq_decode_bytes.argtypes = [vp, i32, i32]
     L.rq_check.restype = i32
@@ -192,6 +198,26 @@ def _check_dev(t, dtype_name: str, shape, what: str):
         raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
+def _out_type(dtype) -> int:
+    import torch
+    if dtype == torch.float32:
+        return RQ_OUT_FP32
+    if dtype == torch.bfloat16:
+        return RQ_OUT_BF16
+    raise ValueError(f"outputs are float32 or bfloat16, got {dtype}")
+
+
+def _check_rows(t, shape, what: str):
+    """A CUDA tensor of rows of HEAD_DIM contiguous elements, the rows at any strides."""
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    _out_type(t.dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.stride(-1) != 1:
+        raise ValueError(f"the last dimension of {what} must be contiguous")
+
+
 def rq_cache_create(cfg: rq_config, arena=None) -> ctypes.c_void_p:
     h = ctypes.c_void_p()
     nbytes = 0 if arena is None else arena.numel() * arena.element_size()
@@ -235,6 +261,12 @@ def rq_prefill_attn(h, layer: int, loop: int, q, n_tokens: int, out, softmax_sca
 def rq_decode_attn_noalloc(h, layer: int, loop: int, q, out, softmax_scale: float = 0.0, stream=None) -> int:
     return lib.rq_decode_attn_noalloc(h, layer, loop, ctypes.c_void_p(_ptr(q)), ctypes.c_void_p(_ptr(out)),
                                       softmax_scale, ctypes.c_void_p(_stream(stream)))
+
+
+def rq_cache_read(h, layer: int, loop: int, t0: int, n_tokens: int, out_type: int, k, v, stride_b: int,
+                  stride_t: int, stride_h: int, stream=None) -> int:
+    return lib.rq_cache_read(h, layer, loop, t0, n_tokens, out_type, ctypes.c_void_p(_ptr(k)),
+                             ctypes.c_void_p(_ptr(v)), stride_b, stride_t, stride_h, ctypes.c_void_p(_stream(stream)))
 
 
 def rq_cache_length(h, layer: int, group: int) -> int:
@@ -312,6 +344,7 @@ class Cache:
         if arena is None and not library_alloc:
             self.arena = torch.empty(self.nbytes, dtype=torch.uint8, device=device or "cuda")
         self.h = rq_cache_create(cfg, self.arena)
+        self.device = self.arena.device if self.arena is not None else torch.device("cuda", torch.cuda.current_device())
 
     def close(self):
         if getattr(self, "h", None):
@@ -367,6 +400,34 @@ class Cache:
         _check_dev(out, "float32", (self.B, self.Hq, HEAD_DIM), "out")
         _ok(rq_append_decode_attn(self.h, layer, loop, k, v, n, q, out, scale, stream), "rq_append_decode_attn")
         return out
+
+    def read(self, layer: int, loop: int, t0: int = 0, n: int | None = None, k=None, v=None, dtype=None,
+             stream=None):
+        """rq_cache_read: tokens t0 .. t0 + n - 1 of (layer, loop) as K and V rows, [batch][n][num_kv_heads][128].
+        k, v: bfloat16 or float32 tensors of that shape and of the same strides (any rows of 128 contiguous
+        elements, 16-byte aligned); rows past a sequence's end are left as they are.  By default new zeroed
+        tensors of `dtype` (bfloat16 unless given), and n runs to the end of the longest sequence."""
+        import torch
+        if (k is None) != (v is None):
+            raise ValueError("give both k and v, or neither")
+        if n is None:
+            bf16 = self.cfg.format == RQ_FMT_BF16
+            n = k.shape[1] if k is not None else (
+                self.length(layer, loop if bf16 else loop // self.Lg) + self.tail_length(layer, loop) - t0)
+        if n < 1 and k is None:
+            raise ValueError(f"no token from {t0} on")
+        if k is None:
+            shape = (self.B, n, self.H, HEAD_DIM)
+            k, v = (torch.zeros(shape, dtype=dtype or torch.bfloat16, device=self.device) for _ in range(2))
+        for x, what in ((k, "k"), (v, "v")):
+            _check_rows(x, (self.B, n, self.H, HEAD_DIM), what)
+        if k.dtype != v.dtype or (dtype is not None and k.dtype != dtype):
+            raise ValueError(f"k and v must have one type{'' if dtype is None else f', {dtype}'}")
+        if k.stride() != v.stride():
+            raise ValueError("k and v must have the same strides")
+        _ok(rq_cache_read(self.h, layer, loop, t0, n, _out_type(k.dtype), k, v, k.stride(0), k.stride(1), k.stride(2),
+                          stream), "rq_cache_read")
+        return k, v
 
     def length(self, layer: int, group: int) -> int:
         return rq_cache_length(self.h, layer, group)

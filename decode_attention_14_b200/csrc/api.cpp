@@ -8,6 +8,7 @@
 #include <new>
 
 #include "prefill.h"
+#include "read.h"
 #include "rq_internal.h"
 
 using namespace rq;
@@ -258,6 +259,23 @@ void grow(rq_cache *c, size_t slot, int n) {
     int *v = seq_lens(c, slot);
     for (int b = 0; b < c->lay.cfg.batch; b++) v[b] += n;
     c->len[slot] += n;
+}
+
+// Whether the rows of kHeadDim elements at b * sb + i * st + h * sh (extents
+// nb, nt, nh) are whole 16-byte vectors (vec elements) that do not overlap:
+// going from the smallest stride to the largest, each is at least the span of
+// the dimensions before it.  The stride of an extent of one does not matter.
+bool rows_disjoint(int64_t nb, int64_t sb, int64_t nt, int64_t st, int64_t nh, int64_t sh, int64_t vec) {
+    std::pair<int64_t, int64_t> d[3] = {{sb, nb}, {st, nt}, {sh, nh}};
+    std::sort(d, d + 3);
+    int64_t span = kHeadDim;
+    for (const auto &x : d) {
+        if (x.second == 1) continue;
+        if (x.first < span || x.first % vec != 0) return false;
+        if (x.first > INT64_MAX / 4 / x.second) return false;
+        span += x.first * (x.second - 1);
+    }
+    return true;
 }
 
 float resolve_scale(float s) { return s > 0.f ? s : 1.0f / std::sqrt((float)kHeadDim); }
@@ -999,6 +1017,66 @@ int rq_cache_export(const rq_cache *c, int layer, int loop, void *host_codes, vo
         if (e != cudaSuccess) return RQ_ERR_CUDA;
     }
     return cuda_status(cudaStreamSynchronize(st));
+}
+
+int rq_cache_read(rq_cache *c, int layer, int loop, int t0, int n, int out_type, void *k_out, void *v_out,
+                  int64_t sb, int64_t st, int64_t sh, void *stream) {
+    if (!c || !k_out || !v_out || k_out == v_out || t0 < 0 || n < 1) return RQ_ERR_INVALID;
+    if (out_type != RQ_OUT_FP32 && out_type != RQ_OUT_BF16) return RQ_ERR_INVALID;
+    if (!on_cache_device(c)) return RQ_ERR_INVALID;
+    const Layout &L = c->lay;
+    const rq_config &cfg = L.cfg;
+    if (layer < 0 || layer >= cfg.num_layers || loop < 0 || loop >= cfg.num_loops) return RQ_ERR_INVALID;
+    if (((uintptr_t)k_out | (uintptr_t)v_out) % 16 != 0) return RQ_ERR_INVALID;
+    const int64_t vec = out_type == RQ_OUT_BF16 ? 8 : 4;   // elements of 16 bytes
+    if (!rows_disjoint(cfg.batch, sb, n, st, cfg.num_kv_heads, sh, vec)) return RQ_ERR_INVALID;
+    ReadArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.out[0] = k_out;
+    a.out[1] = v_out;
+    a.out_type = out_type;
+    a.sb = sb;
+    a.st = st;
+    a.sh = sh;
+    a.B = cfg.batch;
+    a.H = cfg.num_kv_heads;
+    a.t0 = t0;
+    a.tail_cap = L.tail_cap;
+    a.Tp = L.Tp;
+    a.g = cfg.group_size;
+    a.rotate = cfg.rotate;
+    a.pg = pages_of(c);
+    std::memcpy(a.sigma, &c->sigma[(size_t)layer * 4], sizeof(a.sigma));
+    int end;   // of the longest sequence
+    if (cfg.format == RQ_FMT_BF16) {
+        const size_t slot = (size_t)layer * cfg.num_loops + loop;
+        fill_lens(seq_lens(c, slot), cfg.batch, &a.seqT);
+        end = c->len[slot];
+        for (int kv = 0; kv < 2; kv++) a.bf[kv] = bf16_ptr(c, layer, loop, kv);
+    } else {
+        const int group = loop / L.Lg, j = loop % L.Lg;
+        const size_t slot = (size_t)layer * L.groups + group;
+        fill_lens(seq_lens(c, slot), cfg.batch, &a.seqT);
+        if (!is_commit_loop(L, loop)) a.n_tail = c->ntail[(size_t)layer * cfg.num_loops + loop];
+        end = c->len[slot] + a.n_tail;
+        const int rs = record_slot(L, loop);
+        const int r0 = cfg.anchor_mode == 1 ? 0 : rs;
+        a.nr = rs < 0 ? 0 : rs - r0 + 1;
+        a.resid_stride = L.resid_block;
+        for (int kv = 0; kv < 2; kv++) {
+            a.a_codes[kv] = anchor_codes(c, layer, group, kv);
+            a.a_meta[kv] = anchor_meta(c, layer, group, kv);
+            if (a.nr > 0) {
+                a.r_codes[kv] = resid_codes(c, layer, group, r0, kv);
+                a.r_meta[kv] = resid_meta(c, layer, group, r0, kv);
+                a.r_coef[kv] = resid_coef(c, layer, group, r0, kv);
+            }
+            if (a.n_tail > 0) a.tail[kv] = (const uint16_t *)tail_ptr(c, layer, group, j, kv);
+        }
+    }
+    if (t0 >= end) return RQ_OK;   // nothing to write
+    a.n = std::min(n, end - t0);
+    return cuda_status(launch_read(a, cfg.anchor_bits, cfg.resid_bits, (cudaStream_t)stream));
 }
 
 size_t rq_decode_bytes(const rq_cache *c, int layer, int loop) {

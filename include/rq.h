@@ -131,6 +131,13 @@ typedef struct rq_config {
     int32_t num_blocks;
 } rq_config;
 
+/* Element type of the rows a call writes (rq_cache_read and the windowed
+ * attention calls). */
+typedef enum {
+    RQ_OUT_FP32 = 0,
+    RQ_OUT_BF16 = 1           /* the fp32 result rounded once, to nearest even */
+} rq_out_type;
+
 typedef struct rq_cache rq_cache;
 
 /* Human-readable name of a status code (static string). */
@@ -331,6 +338,32 @@ int rq_cache_truncate_seq(rq_cache *cache, int layer, int group, int seq, int ne
  */
 int rq_cache_export(const rq_cache *cache, int layer, int loop, void *host_codes, void *host_meta,
                     void *host_coef, void *stream);
+
+/*
+ * Reads the cache back: the tokens [t0, t0 + n_tokens) of one (layer, loop) of
+ * every sequence as K and V rows in device memory, rebuilt from their records
+ * (the inverse of rq_append up to its quantization; ai4snews summary,
+ * paragraph 3: two reads per token).  Both cache formats, contiguous and
+ * paged, every anchor_mode and loop.
+ *   Tokens of a sequence: its committed tokens of the loop's group (what
+ *     rq_decode_attn sees: s_hat a_hat + R^T r_hat; the anchor loop: a_hat;
+ *     RQ_FMT_BF16: the stored values), then the loop's BF16 tail tokens.
+ *   k_out, v_out: device; token t0 + i, head h, element e of sequence b is
+ *     written to element b * stride_b + i * stride_t + h * stride_h + e of
+ *     each.  Rows at and past a sequence's end (and everything between the
+ *     rows) are left as they are; t0 may lie past the end of every sequence.
+ *   out_type: rq_out_type of the elements.  The values are rebuilt in fp32
+ *     (relative error a few 2^-24 of the largest term) and rounded once.
+ *   Strides are in elements, multiples of 16 bytes, and no two rows overlap;
+ *     k_out and v_out are 16-byte aligned and must not overlap each other.
+ * Reads no memory but the records and the tail, writes no cache state and
+ * uses no workspace: calls on one cache may overlap each other and the
+ * attention calls (not the appends of the tokens read).
+ * Errors: INVALID (null pointer, index, t0 < 0, n_tokens < 1, alignment or
+ * strides), CUDA.
+ */
+int rq_cache_read(rq_cache *cache, int layer, int loop, int t0, int n_tokens, int out_type, void *k_out,
+                  void *v_out, int64_t stride_b, int64_t stride_t, int64_t stride_h, void *stream);
 
 /* Algorithmic bytes one decode call of (layer, loop) moves at the current
  * lengths: codes + FP8 meta + BF16 coefficients of the records read (anchor
