@@ -12,20 +12,30 @@
 // codes, +-1 matrix, fp32 accumulators) gives it exactly for 16 records and 8
 // elements.  H_8 over the segments then adds registers of one thread.
 //
-// Layout.  A warp takes 16 consecutive tokens of one (K|V, sequence, kv head).
-// The columns of the +-1 matrix are permuted so that lane 4 r + q ends with
-// elements 16 g + 4 q .. 16 g + 4 q + 3 of records r and r + 8 for every
-// segment g: H_8 needs no exchange between lanes, and the four lanes of a
+// Layout.  A warp takes 16 consecutive tokens at a time of one (K|V, sequence,
+// kv head).  The columns of the +-1 matrix are permuted so that lane 4 r + q
+// ends with elements 16 g + 4 q .. 16 g + 4 q + 3 of records r and r + 8 for
+// every segment g: H_8 needs no exchange between lanes, and the four lanes of a
 // record write whole 32-byte sectors.  The codes enter the tensor core as
-// 128 + c (bits of a code beside 0x4300 are that BF16 number); the bias comes
-// out as 16 * 128 in element 0 and is taken off by the accumulators' initial
-// value.  The rows (K dimension) are permuted so that two codes of a word 16
+// 128 + c (bits of a code beside 0x4300 are that BF16 number; 2-bit codes of
+// odd elements as 128 + 4 c against +-1/4, which saves a shift); the biases come
+// out in elements 0 and 1 and are taken off by the accumulators' initial
+// values.  The rows (K dimension) are permuted so that two codes of a word 16
 // bits apart are one operand register.
 //
-// fp32 throughout (the codes, FP8 scales and minima are exact in it), rounded
-// once to the output's type.
+// Data movement.  Tiles of 16 tokens are aligned in the sequence, so the 16
+// records of a tile lie behind one another (a block holds 128 or 256 tokens, a
+// contiguous sequence is padded to 64).  Each warp runs through its records (of
+// each tile the residual records, last of the chain first, then the anchor)
+// with a ring of kSlots slots in shared memory, filled ahead by 16-byte
+// asynchronous copies; rows are padded by 16 bytes so that no read of eight
+// records conflicts.
+//
+// fp32 throughout (the codes, FP8 scales and minima are exact in it; two
+// elements per instruction), rounded once to the output's type.
 #include "common.cuh"
 #include "read.h"
+#include "sync.cuh"
 
 namespace rq {
 namespace {
@@ -35,7 +45,16 @@ constexpr int kWarps = 4;                          // warps per CTA
 #ifndef RQ_READ_CTAS
 #define RQ_READ_CTAS 4
 #endif
-constexpr int kRecs = 16;                          // records per warp
+static_assert(32 * kWarps == kHeadDim, "a thread per sign");
+constexpr int kRecs = 16;                          // records of a tile
+#ifndef RQ_READ_TILES
+#define RQ_READ_TILES 2
+#endif
+#ifndef RQ_READ_SLOTS
+#define RQ_READ_SLOTS 4
+#endif
+constexpr int kTiles = RQ_READ_TILES;              // tiles per warp of a large call
+constexpr int kSlots = RQ_READ_SLOTS;              // ring slots per warp: kSlots - 1 steps in flight
 
 // d = a b + c on the tensor cores: a 16 x 16, b 16 x 8, BF16, fp32 sums.
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2],
@@ -47,51 +66,8 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
           "f"(c[3]));
 }
 
-// (scale, minimum) of segment sg of a record's meta bytes.
-template <int GS>
-__device__ __forceinline__ float2 seg_meta(const uint32_t (&m)[GS == 16 ? 4 : 2], int sg) {
-    const int grp = sg * 16 / GS;
-    const uint32_t pr = (m[grp >> 1] >> (16 * (grp & 1))) & 0xFFFFu;
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)pr, __NV_E4M3);
-    return __half22float2(__half2(h));
-}
-template <int GS>
-__device__ __forceinline__ void load_meta(const uint8_t *p, uint32_t (&m)[GS == 16 ? 4 : 2]) {
-    if (GS == 16) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
-        m[0] = v.x;
-        m[1] = v.y;
-        m[GS == 16 ? 2 : 0] = v.z;
-        m[GS == 16 ? 3 : 0] = v.w;
-    } else {
-        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
-        m[0] = v.x;
-        m[1] = v.y;
-    }
-}
-
-// The lane's four codes of segment sg (elements 16 sg + 4 q ..), packed.
-template <int BITS>
-__device__ __forceinline__ uint32_t lane_codes(const uint8_t *codes, int sg, int q) {
-    return BITS == 4 ? (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(codes) + 4 * sg + q)
-                     : (uint32_t)__ldg(codes + 4 * sg + q);
-}
-// sc code + mn of those four: 128 + c as a float is the code's bits beside
-// 0x43000000, and sc (128 + c) + (mn - 128 sc) is one rounding away from it.
-template <int BITS>
-__device__ __forceinline__ void expand4(uint32_t w, float2 sm, float x[4]) {
-    const float off = fmaf(-128.f, sm.x, sm.y);
-#pragma unroll
-    for (int k = 0; k < 4; k++) {
-        constexpr uint32_t mask = (uint32_t)((1 << BITS) - 1) << 16;
-        const int sh = 16 - k * BITS;
-        const uint32_t c = (sh >= 0 ? w << sh : w >> -sh) & mask;
-        x[k] = fmaf(sm.x, __uint_as_float(c | 0x43000000u), off);
-    }
-}
-
 template <int OUT>
-__device__ __forceinline__ void store4(void *out, size_t at, const float x[4]) {
+__device__ __forceinline__ void store4(void *out, long long at, const float x[4]) {
     if (OUT == RQ_OUT_BF16) {
         const __nv_bfloat162 lo = __floats2bfloat162_rn(x[0], x[1]), hi = __floats2bfloat162_rn(x[2], x[3]);
         *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + at) =
@@ -103,220 +79,405 @@ __device__ __forceinline__ void store4(void *out, size_t at, const float x[4]) {
 
 // One row of BF16 values (a tail token, or a token of a BF16 cache) by a warp.
 template <int OUT>
-__device__ __forceinline__ void copy_row(void *out, size_t at, const uint16_t *row, int lane) {
+__device__ __forceinline__ void copy_row(void *out, long long at, const uint16_t *row, int lane) {
     const uint2 w = *reinterpret_cast<const uint2 *>(row + 4 * lane);
     const float x[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
                         __uint_as_float(w.y & 0xFFFF0000u)};
     store4<OUT>(out, at + 4 * lane, x);
 }
 
-// The tile of 16 tokens of this warp: (kv, b, h) and the first token's index.
-struct Tile {
-    int kv, b, h, i0;
+// What a warp reads: tiles [tile0, tile0 + tiles) of 16 tokens of one
+// (kv, b, h), of those that hold the call's tokens.
+struct Span {
+    int kv, b, h, tile0, tiles;
 };
-__device__ __forceinline__ bool tile_of(const ReadArgs &a, Tile &t) {
-    const long long wid = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int per = (a.n + kRecs - 1) / kRecs;
-    if (wid >= 2LL * a.B * a.H * per) return false;   // uniform per warp
-    long long r = wid;
-    t.i0 = (int)(r % per) * kRecs;
-    r /= per;
-    t.h = (int)(r % a.H);
-    r /= a.H;
-    t.b = (int)(r % a.B);
-    t.kv = (int)(r / a.B);
-    return true;
+__host__ __device__ inline int tiles_of(int t0, int n) { return (t0 + n - 1) / kRecs - t0 / kRecs + 1; }
+__device__ __forceinline__ bool span_of(const ReadArgs &a, Span &s) {
+    const int nt = tiles_of(a.t0, a.n), per = a.tiles * kWarps, chunks = (nt + per - 1) / per;
+    unsigned u = blockIdx.x / (unsigned)chunks;
+    const int first = ((blockIdx.x - u * chunks) * kWarps + (threadIdx.x >> 5)) * a.tiles;
+    s.tile0 = a.t0 / kRecs + first;
+    s.tiles = min(a.tiles, nt - first);
+    s.h = (int)(u % a.H);
+    u /= a.H;
+    s.b = (int)(u % a.B);
+    s.kv = (int)(u / a.B);
+    return s.tiles > 0;   // uniform per warp
 }
-__device__ __forceinline__ size_t row_at(const ReadArgs &a, const Tile &t, int i) {
-    return (size_t)(t.b * a.sb + i * a.st + t.h * a.sh);
+// Where token t (t0 <= t < t0 + n) of the span's sequence goes.
+__device__ __forceinline__ long long row_at(const ReadArgs &a, const Span &s, int t) {
+    return s.b * a.sb + (t - a.t0) * a.st + s.h * a.sh;
 }
 
-template <int BA, int BR, int GS, bool ROT, int OUT>
-__global__ void __launch_bounds__(32 * kWarps, RQ_READ_CTAS) read_rq_kernel(const ReadArgs a) {
-    const int lane = threadIdx.x & 31, q = lane & 3;
-    Tile tl;
-    if (!tile_of(a, tl)) return;
-    const int T = a.seqT.v[tl.b];
-    const int cnt = min(kRecs, a.n - tl.i0);       // tokens of the tile
-    const int t0 = a.t0 + tl.i0;
-    const int nc = min(cnt, T - t0);               // of them committed
-    // tail tokens, a row at a time
-    for (int i = max(0, nc); i < cnt && t0 + i < T + a.n_tail; i++) {
-        const uint16_t *row = a.tail[tl.kv] + (((size_t)tl.b * a.tail_cap + (t0 + i - T)) * a.H + tl.h) * kHeadDim;
-        copy_row<OUT>(a.out[tl.kv], row_at(a, tl, tl.i0 + i), row, lane);
-    }
-    if (nc <= 0) return;
+__device__ __forceinline__ void async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void async8(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
-    constexpr int MR = 2 * (kHeadDim / GS), NM = GS == 16 ? 4 : 2;
-    // the lane's two records; a row past the committed ones repeats the last
-    const int row[2] = {lane >> 2, (lane >> 2) + 8};
-    size_t rec[2];
+// Two fp32 operations per instruction.
+struct F2 {
+    unsigned long long v;
+};
+__device__ __forceinline__ F2 pack2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(F2 p, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p.v)); }
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
+// A ring slot: codes of 16 records (rows padded by 16 bytes), then their meta.
+template <int BA, int BR>
+struct Slot {
+    static constexpr int pitch(int bits) { return 16 * bits + 16; }
+    static constexpr int META = kRecs * pitch(BA > BR ? BA : BR);
+    static constexpr int BYTES = META + kRecs * 16;
+};
+
+// Codes and meta of the 16 records from row rec on into a slot.
+template <int BITS, int GS>
+__device__ __forceinline__ void fetch(uint32_t slot, int meta_off, const uint8_t *codes, const uint8_t *meta,
+                                      size_t rec, int lane) {
+    constexpr int MR = 2 * (kHeadDim / GS);
+    const uint8_t *src = codes + rec * (16 * BITS) + lane * 16;
 #pragma unroll
-    for (int u = 0; u < 2; u++) rec[u] = rec_row(a.pg, a.H, tl.b, tl.h, t0 + min(row[u], nc - 1));
+    for (int i = 0; i < BITS / 2; i++) {   // 32 chunks a round, BITS chunks a record
+        const int ch = i * 32 + lane;
+        async16(slot + (ch / BITS) * (16 * BITS + 16) + (ch % BITS) * 16, src + i * 512);
+    }
+    if (lane < kRecs) {
+        if (MR == 16) async16(slot + meta_off + lane * 16, meta + rec * MR + lane * 16);
+        else async8(slot + meta_off + lane * 16, meta + rec * MR + lane * 8);
+    }
+}
+
+// (scale, minimum) of segment sg of a record's meta bytes.
+template <int GS>
+__device__ __forceinline__ float2 seg_meta(const uint4 &m, int sg) {
+    const int grp = sg * 16 / GS;
+    const uint32_t w = (grp >> 1) == 0 ? m.x : (grp >> 1) == 1 ? m.y : (grp >> 1) == 2 ? m.z : m.w;
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)((w >> (16 * (grp & 1))) & 0xFFFFu), __NV_E4M3);
+    return __half22float2(__half2(h));
+}
+
+// The lane's four values sc c + mn of segment sg of a record (elements
+// 16 sg + 4 q ..).  A code's bits at position p of the low mantissa beside the
+// exponent of 2^(23 - p) are the float 2^(23 - p) + c, exactly.
+template <int BITS>
+__device__ __forceinline__ void expand4(const uint8_t *row, int sg, int q, float2 sm, F2 (&x)[2]) {
+    const uint32_t w = BITS == 4 ? (uint32_t)reinterpret_cast<const uint16_t *>(row)[4 * sg + q] : (uint32_t)row[4 * sg + q];
+    float f[4], e[4];
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        const uint32_t ex = (uint32_t)(127 + 23 - k * BITS) << 23;
+        f[k] = __uint_as_float((w & ((uint32_t)((1 << BITS) - 1) << (k * BITS))) | ex);
+        e[k] = -__uint_as_float(ex);
+    }
+    const F2 sc = pack2(sm.x, sm.x), mn = pack2(sm.y, sm.y);
+    x[0] = fma2(sc, add2(pack2(f[0], f[1]), pack2(e[0], e[1])), mn);
+    x[1] = fma2(sc, add2(pack2(f[2], f[3]), pack2(e[2], e[3])), mn);
+}
+
+// NR: residual records read, 0 or 1 (the shared reference), or 2 for any
+// number (a.nr, the chained reference).
+template <int BA, int BR, int GS, int NR, bool ROT, int OUT>
+__global__ void __launch_bounds__(32 * kWarps, NR == 2 ? 3 : RQ_READ_CTAS) read_rq_kernel(const ReadArgs a) {
+    using S = Slot<BA, BR>;
+    const int nr = NR < 2 ? NR : a.nr;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ __align__(16) float s_sign[kHeadDim];   // sigma / sqrt(d)
+    const int lane = threadIdx.x & 31, q = lane & 3;
+    if (ROT) {
+        s_sign[threadIdx.x] = sigma_neg(a.sigma, threadIdx.x) ? -kRsqrtD : kRsqrtD;
+        __syncthreads();
+    }
+    Span sp;
+    if (!span_of(a, sp)) return;
+    const int T = a.seqT.v[sp.b];
+    // the span's tokens: [lo, hi) of the call, of them [lo, mid) committed
+    const int lo = max(a.t0, sp.tile0 * kRecs);
+    const int hi = min(min(a.t0 + a.n, (sp.tile0 + sp.tiles) * kRecs), T + a.n_tail), mid = min(hi, T);
+    // tail tokens, a row at a time
+    for (int t = max(lo, mid); t < hi; t++) {
+        const uint16_t *row = a.tail[sp.kv] + (((size_t)sp.b * a.tail_cap + (t - T)) * a.H + sp.h) * kHeadDim;
+        copy_row<OUT>(a.out[sp.kv], row_at(a, sp, t), row, lane);
+    }
+    if (mid <= lo) return;
+
+    uint8_t *ring = smem + (threadIdx.x >> 5) * (kSlots * S::BYTES);
+    const uint32_t ring_s = smem_u32(ring);
+    const int tiles = (mid - 1) / kRecs - sp.tile0 + 1, nstep = tiles * (nr + 1);
+    // the step being fetched: tile ft, record fk of the chain (-1: the anchor),
+    // slot fs; its first row and, for residual records, the coefficients (lane
+    // r keeps record r's until the step is consumed)
+    int ft = 0, fk = nr - 1, fs = 0, fstep = 0;
+    size_t frec = 0;
+    uint32_t coef[kSlots];
+    auto fetch_next = [&](uint32_t &cf) {
+        if (fstep < nstep) {
+            if (fk == nr - 1)   // a new tile
+                frec = rec_row(a.pg, a.H, sp.b, sp.h, (sp.tile0 + ft) * kRecs);
+            const uint32_t slot = ring_s + fs * S::BYTES;
+            if (fk >= 0) {
+                const size_t o = fk * a.resid_stride;
+                fetch<BR, GS>(slot, S::META, a.r_codes[sp.kv] + o, a.r_meta[sp.kv] + o, frec, lane);
+                cf = __ldg(reinterpret_cast<const uint16_t *>(a.r_coef[sp.kv] + o) + frec + (lane & 15));
+                fk--;
+            } else {
+                fetch<BA, GS>(slot, S::META, a.a_codes[sp.kv], a.a_meta[sp.kv], frec, lane);
+                fk = nr - 1;
+                ft++;
+            }
+            fstep++;
+            fs = fs + 1 == kSlots ? 0 : fs + 1;
+        }
+        async_commit();
+    };
+    // coefficients rotate through registers with the slots: coef[0] is the
+    // step's being consumed
+#pragma unroll
+    for (int i = 0; i < kSlots - 1; i++) {
+        coef[i] = 0;
+        fetch_next(coef[i]);
+    }
+
+    // +-1 operand: column lane / 4 of output half nt is element
+    // 4 (col / 2) + 2 nt + col % 2; row slots 2 q, 2 q + 1, 2 q + 8, 2 q + 9
+    // are elements 2 q, 2 q + 8, 2 q + 1, 2 q + 9
+    uint32_t hm[2][2];
+    float init[2][4];
+    if (ROT) {
+        const int col = lane >> 2;
+#pragma unroll
+        for (int nt = 0; nt < 2; nt++) {
+            const int e = 4 * (col >> 1) + 2 * nt + (col & 1);
+#pragma unroll
+            for (int s = 0; s < 2; s++) {
+                const uint32_t one = BR == 2 && s == 1 ? 0x3E80u : 0x3F80u;   // 1/4 or 1
+                const uint32_t x = (__popc((2 * q + s) & e) & 1) ? one | 0x8000u : one;
+                const uint32_t y = (__popc((2 * q + s + 8) & e) & 1) ? one | 0x8000u : one;
+                hm[nt][s] = x | (y << 16);
+            }
+        }
+        // biases: 8 rows of 128 and 8 of 128 / 4 (or 128), summed in element
+        // 0 and, even rows against odd, in element 1
+        const float odd = BR == 2 ? 32.f : 128.f;
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            init[0][k] = q == 0 ? ((k & 1) ? -8.f * (128.f - odd) : -8.f * (128.f + odd)) : 0.f;
+            init[1][k] = 0.f;
+        }
+    }
+    const float e0 = q == 0 ? 16.f : 0.f;   // the lanes that hold element 0 of every segment
+    const F2 neg1 = pack2(-1.f, -1.f);
 
     // z = sum_k c_k y_k over the residual records, c_k the product of the
     // coefficients of the records after k (1 for the last): the chain
     // x <- s_k x + R^T y_k unrolled, so that the anchor gets the product of
     // all of them and R^T is applied once.  Under ROT z holds H_16 z_g.
-    float z[2][8][4], c[2] = {1.f, 1.f};
-#pragma unroll
-    for (int u = 0; u < 2; u++)
-#pragma unroll
-        for (int sg = 0; sg < 8; sg++)
-#pragma unroll
-            for (int e = 0; e < 4; e++) z[u][sg][e] = 0.f;
-    if (a.nr > 0) {
-        // +-1 operand: column lane / 4 of output half nt is element
-        // 4 (col / 2) + 2 nt + col % 2; row slots 2 q, 2 q + 1, 2 q + 8, 2 q + 9
-        // are elements 2 q, 2 q + 8, 2 q + 1, 2 q + 9
-        uint32_t hm[2][2];
-        float init[2][4];
-        if (ROT) {
-            const int col = lane >> 2;
-#pragma unroll
-            for (int nt = 0; nt < 2; nt++) {
-                const int e = 4 * (col >> 1) + 2 * nt + (col & 1);
-#pragma unroll
-                for (int s = 0; s < 2; s++) {
-                    const uint32_t lo = (__popc((2 * q + s) & e) & 1) ? 0xBF80u : 0x3F80u;
-                    const uint32_t hi = (__popc((2 * q + s + 8) & e) & 1) ? 0xBF80u : 0x3F80u;
-                    hm[nt][s] = lo | (hi << 16);
-                }
-#pragma unroll
-                for (int k = 0; k < 4; k++) init[nt][k] = (nt == 0 && q == 0 && (k & 1) == 0) ? -2048.f : 0.f;
-            }
-        }
-        const float e0 = q == 0 ? 16.f : 0.f;   // the lanes that hold element 0 of every segment
+    int cs = 0;   // slot consumed
 #pragma unroll 1
-        for (int k = a.nr - 1; k >= 0; k--) {
-            const size_t o = k * a.resid_stride;
-            uint32_t m[2][NM];
+    for (int tile = 0; tile < tiles; tile++) {
+        F2 z[2][8][2];
+        float c[2] = {1.f, 1.f};
+        if (nr > 0) {
+#pragma unroll 1
+            for (int k = nr - 1; k >= 0; k--) {
+                async_wait<kSlots - 2>();
+                __syncwarp();
+                const uint8_t *st = ring + cs * S::BYTES;
+                uint4 m[2];
+                const uint8_t *cp[2];
 #pragma unroll
-            for (int u = 0; u < 2; u++) load_meta<GS>(a.r_meta[tl.kv] + o + rec[u] * MR, m[u]);
-            const uint8_t *cp[2] = {a.r_codes[tl.kv] + o + rec[0] * (16 * BR), a.r_codes[tl.kv] + o + rec[1] * (16 * BR)};
-            uint16_t sb[2];
+                for (int u = 0; u < 2; u++) {
+                    const int r = (lane >> 2) + 8 * u;
+                    m[u] = *reinterpret_cast<const uint4 *>(st + S::META + 16 * r);
+                    cp[u] = st + r * S::pitch(BR);
+                }
+                const bool first = NR < 2 || k == nr - 1;
 #pragma unroll
-            for (int u = 0; u < 2; u++) sb[u] = __ldg(reinterpret_cast<const uint16_t *>(a.r_coef[tl.kv] + o) + rec[u]);
+                for (int sg = 0; sg < 8; sg++) {
+                    F2 y[2][2];
+                    if (ROT) {
+                        uint32_t av[4];
 #pragma unroll
-            for (int sg = 0; sg < 8; sg++) {
-                float y[2][4];
-                if (ROT) {
-                    uint32_t av[4];
-#pragma unroll
-                    for (int u = 0; u < 2; u++) {
-                        if (BR == 2) {   // element k at bits 2 k of the segment's word
-                            const uint32_t v = __ldg(reinterpret_cast<const uint32_t *>(cp[u]) + sg) >> (4 * q);
-                            av[u] = (v & 0x00030003u) | 0x43004300u;              // elements 2q, 2q + 8
-                            av[2 + u] = ((v >> 2) & 0x00030003u) | 0x43004300u;   // 2q + 1, 2q + 9
-                        } else {         // elements 0-7 and 8-15 in two words: byte q of each
-                            const uint2 w = __ldg(reinterpret_cast<const uint2 *>(cp[u]) + sg);
-                            const uint32_t v = __byte_perm(w.x, w.y, (uint32_t)(q | ((4 + q) << 8)));   // into bytes 0, 2
-                            av[u] = (v & 0x000F000Fu) | 0x43004300u;
-                            av[2 + u] = ((v >> 4) & 0x000F000Fu) | 0x43004300u;
+                        for (int u = 0; u < 2; u++) {
+                            if (BR == 2) {   // element k at bits 2 k of the segment's word
+                                const uint32_t v = reinterpret_cast<const uint32_t *>(cp[u])[sg] >> (4 * q);
+                                av[u] = (v & 0x00030003u) | 0x43004300u;              // elements 2q, 2q + 8
+                                av[2 + u] = (v & 0x000C000Cu) | 0x43004300u;          // 2q + 1, 2q + 9, times 4
+                            } else {         // elements 0-7 and 8-15 in two words: byte q of each, into bytes 0, 2
+                                const uint2 w = reinterpret_cast<const uint2 *>(cp[u])[sg];
+                                const uint32_t v = __byte_perm(w.x, w.y, (uint32_t)(q | ((4 + q) << 8)));
+                                av[u] = (v & 0x000F000Fu) | 0x43004300u;
+                                av[2 + u] = ((v >> 4) & 0x000F000Fu) | 0x43004300u;
+                            }
                         }
-                    }
-                    float d0[4], d1[4];
-                    mma16816(d0, av, hm[0], init[0]);
-                    mma16816(d1, av, hm[1], init[1]);
+                        float d0[4], d1[4];
+                        mma16816(d0, av, hm[0], init[0]);
+                        mma16816(d1, av, hm[1], init[1]);
 #pragma unroll
-                    for (int u = 0; u < 2; u++) {
-                        const float2 sm = seg_meta<GS>(m[u], sg);
-                        y[u][0] = fmaf(sm.x, d0[2 * u], e0 * sm.y);
-                        y[u][1] = sm.x * d0[2 * u + 1];
-                        y[u][2] = sm.x * d1[2 * u];
-                        y[u][3] = sm.x * d1[2 * u + 1];
-                    }
-                } else {
+                        for (int u = 0; u < 2; u++) {
+                            const float2 sm = seg_meta<GS>(m[u], sg);
+                            const F2 sc = pack2(sm.x, sm.x);
+                            y[u][0] = fma2(sc, pack2(d0[2 * u], d0[2 * u + 1]), pack2(e0 * sm.y, 0.f));
+                            y[u][1] = mul2(sc, pack2(d1[2 * u], d1[2 * u + 1]));
+                        }
+                    } else {
 #pragma unroll
-                    for (int u = 0; u < 2; u++) expand4<BR>(lane_codes<BR>(cp[u], sg, q), seg_meta<GS>(m[u], sg), y[u]);
+                        for (int u = 0; u < 2; u++) expand4<BR>(cp[u], sg, q, seg_meta<GS>(m[u], sg), y[u]);
+                    }
+#pragma unroll
+                    for (int u = 0; u < 2; u++)
+#pragma unroll
+                        for (int e = 0; e < 2; e++)
+                            z[u][sg][e] = first ? y[u][e] : fma2(pack2(c[u], c[u]), y[u][e], z[u][sg][e]);
                 }
 #pragma unroll
                 for (int u = 0; u < 2; u++)
+                    c[u] *= bf16_to_f32((uint16_t)__shfl_sync(0xffffffffu, coef[0], (lane >> 2) + 8 * u));
+                __syncwarp();
 #pragma unroll
-                    for (int e = 0; e < 4; e++) z[u][sg][e] = fmaf(c[u], y[u][e], z[u][sg][e]);
+                for (int i = 0; i + 1 < kSlots - 1; i++) coef[i] = coef[i + 1];
+                fetch_next(coef[kSlots - 2]);
+                cs = cs + 1 == kSlots ? 0 : cs + 1;
             }
+            if (ROT) {   // H_8 over the segments
 #pragma unroll
-            for (int u = 0; u < 2; u++) c[u] *= bf16_to_f32(sb[u]);
+                for (int g = 1; g < 8; g <<= 1)
+#pragma unroll
+                    for (int sg = 0; sg < 8; sg++)
+                        if ((sg & g) == 0) {
+#pragma unroll
+                            for (int u = 0; u < 2; u++)
+#pragma unroll
+                                for (int e = 0; e < 2; e++) {
+                                    const F2 p = z[u][sg][e], r = z[u][sg + g][e];
+                                    z[u][sg][e] = add2(p, r);
+                                    z[u][sg + g][e] = fma2(r, neg1, p);
+                                }
+                        }
+            }
         }
-        if (ROT) {   // H_8 over the segments
+        // x = c a + diag(sigma) z / sqrt(d)
+        async_wait<kSlots - 2>();
+        __syncwarp();
+        const uint8_t *st = ring + cs * S::BYTES;
+        uint4 m[2];
+        long long at[2];
+        bool in[2];
 #pragma unroll
-            for (int w = 1; w < 8; w <<= 1)
-#pragma unroll
-                for (int sg = 0; sg < 8; sg++)
-                    if ((sg & w) == 0) {
-#pragma unroll
-                        for (int u = 0; u < 2; u++)
-#pragma unroll
-                            for (int e = 0; e < 4; e++) {
-                                const float p = z[u][sg][e], r = z[u][sg + w][e];
-                                z[u][sg][e] = p + r;
-                                z[u][sg + w][e] = p - r;
-                            }
-                    }
+        for (int u = 0; u < 2; u++) {
+            const int r = (lane >> 2) + 8 * u, t = (sp.tile0 + tile) * kRecs + r;
+            m[u] = *reinterpret_cast<const uint4 *>(st + S::META + 16 * r);
+            at[u] = row_at(a, sp, t) + 4 * q;
+            in[u] = t >= lo && t < mid;
         }
-    }
-    // x = c a + diag(sigma) z / sqrt(d)
-#pragma unroll
-    for (int u = 0; u < 2; u++) {
-        uint32_t m[NM];
-        load_meta<GS>(a.a_meta[tl.kv] + rec[u] * MR, m);
-        const uint8_t *codes = a.a_codes[tl.kv] + rec[u] * (16 * BA);
-        const size_t at = row_at(a, tl, tl.i0 + row[u]) + 4 * q;
 #pragma unroll
         for (int sg = 0; sg < 8; sg++) {
-            float x[4];
-            expand4<BA>(lane_codes<BA>(codes, sg, q), seg_meta<GS>(m, sg), x);
-            const uint32_t sig = a.sigma[sg >> 1] >> (16 * (sg & 1) + 4 * q);   // signs of the lane's four elements
+            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (ROT) f = *reinterpret_cast<const float4 *>(s_sign + 16 * sg + 4 * q);
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const float f = ROT ? __uint_as_float(__float_as_uint(kRsqrtD) | ((sig << (31 - e)) & 0x80000000u)) : 1.f;
-                x[e] = fmaf(c[u], x[e], ROT ? z[u][sg][e] * f : z[u][sg][e]);
+            for (int u = 0; u < 2; u++) {
+                F2 x[2];
+                expand4<BA>(st + ((lane >> 2) + 8 * u) * S::pitch(BA), sg, q, seg_meta<GS>(m[u], sg), x);
+                if (nr > 0) {
+                    const F2 cc = pack2(c[u], c[u]);
+                    x[0] = fma2(cc, x[0], ROT ? mul2(z[u][sg][0], pack2(f.x, f.y)) : z[u][sg][0]);
+                    x[1] = fma2(cc, x[1], ROT ? mul2(z[u][sg][1], pack2(f.z, f.w)) : z[u][sg][1]);
+                }
+                float o[4];
+                unpack2(x[0], o[0], o[1]);
+                unpack2(x[1], o[2], o[3]);
+                if (in[u]) store4<OUT>(a.out[sp.kv], at[u] + 16 * sg, o);
             }
-            if (row[u] < nc) store4<OUT>(a.out[tl.kv], at + 16 * sg, x);
         }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i + 1 < kSlots - 1; i++) coef[i] = coef[i + 1];
+        fetch_next(coef[kSlots - 2]);
+        cs = cs + 1 == kSlots ? 0 : cs + 1;
     }
+    async_wait<0>();
 }
 
 template <int OUT>
 __global__ void __launch_bounds__(32 * kWarps) read_bf16_kernel(const ReadArgs a) {
-    Tile tl;
-    if (!tile_of(a, tl)) return;
-    const int lane = threadIdx.x & 31, T = a.seqT.v[tl.b], cnt = min(kRecs, a.n - tl.i0), t0 = a.t0 + tl.i0;
-    const uint16_t *base = a.bf[tl.kv] + (((size_t)tl.b * a.H + tl.h) * a.Tp + t0) * kHeadDim;
+    Span sp;
+    if (!span_of(a, sp)) return;
+    const int lane = threadIdx.x & 31;
+    const int lo = max(a.t0, sp.tile0 * kRecs);
+    const int hi = min(min(a.t0 + a.n, (sp.tile0 + sp.tiles) * kRecs), a.seqT.v[sp.b]);
+    const uint16_t *base = a.bf[sp.kv] + ((size_t)sp.b * a.H + sp.h) * a.Tp * kHeadDim;
 #pragma unroll 4
-    for (int i = 0; i < cnt && t0 + i < T; i++)
-        copy_row<OUT>(a.out[tl.kv], row_at(a, tl, tl.i0 + i), base + (size_t)i * kHeadDim, lane);
+    for (int t = lo; t < hi; t++)
+        copy_row<OUT>(a.out[sp.kv], row_at(a, sp, t), base + (size_t)t * kHeadDim, lane);
 }
 
-template <int BA, int BR, int GS, bool ROT>
-void launch_out(const ReadArgs &a, unsigned blocks, cudaStream_t st) {
-    if (a.out_type == RQ_OUT_BF16)
-        read_rq_kernel<BA, BR, GS, ROT, RQ_OUT_BF16><<<blocks, 32 * kWarps, 0, st>>>(a);
-    else
-        read_rq_kernel<BA, BR, GS, ROT, RQ_OUT_FP32><<<blocks, 32 * kWarps, 0, st>>>(a);
+template <int BA, int BR, int GS, int NR, bool ROT, int OUT>
+cudaError_t launch_t(const ReadArgs &a, unsigned blocks, cudaStream_t st) {
+    constexpr int smem = kWarps * kSlots * Slot<BA, BR>::BYTES;
+    static_assert(smem <= 48 * 1024, "no opt-in needed");
+    read_rq_kernel<BA, BR, GS, NR, ROT, OUT><<<blocks, 32 * kWarps, smem, st>>>(a);
+    return cudaGetLastError();
+}
+template <int BA, int BR, int GS, int NR, bool ROT>
+cudaError_t launch_out(const ReadArgs &a, unsigned blocks, cudaStream_t st) {
+    return a.out_type == RQ_OUT_BF16 ? launch_t<BA, BR, GS, NR, ROT, RQ_OUT_BF16>(a, blocks, st)
+                                     : launch_t<BA, BR, GS, NR, ROT, RQ_OUT_FP32>(a, blocks, st);
+}
+template <int BA, int BR, int GS>
+cudaError_t launch_chain(const ReadArgs &a, unsigned blocks, cudaStream_t st) {
+    if (a.nr == 0) return launch_out<BA, 2, GS, 0, false>(a, blocks, st);
+    if (a.nr == 1)
+        return a.rotate ? launch_out<BA, BR, GS, 1, true>(a, blocks, st) : launch_out<BA, BR, GS, 1, false>(a, blocks, st);
+    return a.rotate ? launch_out<BA, BR, GS, 2, true>(a, blocks, st) : launch_out<BA, BR, GS, 2, false>(a, blocks, st);
 }
 template <int BA, int BR>
-void launch_bits(const ReadArgs &a, unsigned blocks, cudaStream_t st) {
-    const bool rot = a.rotate != 0;
-    if (a.g == 16) rot ? launch_out<BA, BR, 16, true>(a, blocks, st) : launch_out<BA, BR, 16, false>(a, blocks, st);
-    else rot ? launch_out<BA, BR, 32, true>(a, blocks, st) : launch_out<BA, BR, 32, false>(a, blocks, st);
+cudaError_t launch_bits(const ReadArgs &a, unsigned blocks, cudaStream_t st) {
+    return a.g == 16 ? launch_chain<BA, BR, 16>(a, blocks, st) : launch_chain<BA, BR, 32>(a, blocks, st);
 }
 
 }  // namespace
 
-cudaError_t launch_read(const ReadArgs &a, int ba, int br, cudaStream_t st) {
-    const long long warps = 2LL * a.B * a.H * ((a.n + kRecs - 1) / kRecs);
-    const long long blocks = (warps + kWarps - 1) / kWarps;
+cudaError_t launch_read(const ReadArgs &args, int ba, int br, cudaStream_t st) {
+    ReadArgs a = args;
+    const long long units = 2LL * a.B * a.H, nt = tiles_of(a.t0, a.n);
+    // two tiles a warp share its set-up and overlap; one while that leaves
+    // fewer warps than the 148 SMs hold (16 each)
+    a.tiles = units * nt <= 148 * 16 * 2 ? 1 : kTiles;
+    const int per = a.tiles * kWarps;
+    const long long blocks = units * ((nt + per - 1) / per);
     if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
     const unsigned nb = (unsigned)blocks;
-    if (a.bf[0])
+    if (a.bf[0]) {
         a.out_type == RQ_OUT_BF16 ? read_bf16_kernel<RQ_OUT_BF16><<<nb, 32 * kWarps, 0, st>>>(a)
                                   : read_bf16_kernel<RQ_OUT_FP32><<<nb, 32 * kWarps, 0, st>>>(a);
-    else if (ba == 4)
-        br == 2 ? launch_bits<4, 2>(a, nb, st) : launch_bits<4, 4>(a, nb, st);
-    else
-        br == 2 ? launch_bits<2, 2>(a, nb, st) : launch_bits<2, 4>(a, nb, st);
-    return cudaGetLastError();
+        return cudaGetLastError();
+    }
+    if (ba == 4) return br == 2 ? launch_bits<4, 2>(a, nb, st) : launch_bits<4, 4>(a, nb, st);
+    return br == 2 ? launch_bits<2, 2>(a, nb, st) : launch_bits<2, 4>(a, nb, st);
 }
 
 }  // namespace rq

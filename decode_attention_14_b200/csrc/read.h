@@ -24,6 +24,7 @@ struct ReadArgs {
     SeqLens seqT;                      // committed tokens of each sequence
     Pages pg;
     int B, H, t0, n, n_tail, tail_cap, Tp;
+    int tiles;                         // 16-token tiles per warp (set by launch_read)
     int g;
     int rotate;
     uint32_t sigma[4];
