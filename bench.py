@@ -42,7 +42,7 @@ CONFIG_SEED = {"tiny": 0x5EED0000, "ouro8k_b4": 0x5EED0001, "long16k_b2": 0x5EED
 FILL_CHUNK = 512
 
 
-KERNEL_SOURCES = ["decode_attention_14_b200/csrc/decode_rq.cu", "decode_attention_14_b200/csrc/combine.cuh",
+KERNEL_SOURCES = ["decode_attention_14_b200/csrc/decode_rq.cuh", "decode_attention_14_b200/csrc/combine.cuh",
                   "decode_attention_14_b200/csrc/common.cuh", "decode_attention_14_b200/csrc/rq_internal.h"]
 
 

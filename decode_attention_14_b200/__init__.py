@@ -107,6 +107,8 @@ def _load() -> ctypes.CDLL:
     L.rq_cache_length_seq.argtypes = [vp, i32, i32, i32, ctypes.POINTER(i32)]
     L.rq_cache_export.restype = i32
     L.rq_cache_export.argtypes = [vp, i32, i32, vp, vp, vp, vp]
+    L.rq_decode_attn_window.restype = i32
+    L.rq_decode_attn_window.argtypes = [vp, i32, i32, vp, vp, i32, ctypes.c_float, i32, i32, vp]
     i64 = ctypes.c_int64
     L.rq_cache_read.restype = i32
     L.rq_cache_read.argtypes = [vp, i32, i32, i32, i32, i32, vp, vp, i64, i64, i64, vp]
@@ -263,6 +265,12 @@ def rq_decode_attn_noalloc(h, layer: int, loop: int, q, out, softmax_scale: floa
                                       softmax_scale, ctypes.c_void_p(_stream(stream)))
 
 
+def rq_decode_attn_window(h, layer: int, loop: int, q, out, out_type: int, softmax_scale: float, window: int,
+                          sinks: int, stream=None) -> int:
+    return lib.rq_decode_attn_window(h, layer, loop, ctypes.c_void_p(_ptr(q)), ctypes.c_void_p(_ptr(out)), out_type,
+                                     softmax_scale, window, sinks, ctypes.c_void_p(_stream(stream)))
+
+
 def rq_cache_read(h, layer: int, loop: int, t0: int, n_tokens: int, out_type: int, k, v, stride_b: int,
                   stride_t: int, stride_h: int, stream=None) -> int:
     return lib.rq_cache_read(h, layer, loop, t0, n_tokens, out_type, ctypes.c_void_p(_ptr(k)),
@@ -373,6 +381,28 @@ class Cache:
         _check_dev(out, "float32", (self.B, self.Hq, HEAD_DIM), "out")
         fn = rq_decode_attn_bf16 if bf16 else rq_decode_attn
         _ok(fn(self.h, layer, loop, q, out, scale, stream), fn.__name__)
+        return out
+
+    def decode_window(self, layer: int, loop: int, q, window: int, sinks: int = 0, out=None, dtype=None,
+                      scale: float = 0.0, stream=None):
+        """rq_decode_attn_window: the last `window` tokens (0: all) and the first `sinks` ones, over either cache
+        format; q [batch][num_q_heads][128] bf16 -> `dtype` (float32 unless given, or bfloat16) of the same shape."""
+        import torch
+        shape = (self.B, self.Hq, HEAD_DIM)
+        _check_dev(q, "bfloat16", shape, "q")
+        out = self._window_out(out, dtype, shape, q)
+        _ok(rq_decode_attn_window(self.h, layer, loop, q, out, _out_type(out.dtype), scale, window, sinks, stream),
+            "rq_decode_attn_window")
+        return out
+
+    @staticmethod
+    def _window_out(out, dtype, shape, q):
+        import torch
+        if out is None:
+            return torch.empty(shape, dtype=dtype or torch.float32, device=q.device)
+        if dtype is not None and out.dtype != dtype:
+            raise ValueError(f"out is {out.dtype}, not {dtype}")
+        _check_dev(out, "bfloat16" if out.dtype == torch.bfloat16 else "float32", shape, "out")
         return out
 
     def prefill(self, layer: int, loop: int, q, out=None, scale: float = 0.0, stream=None):

@@ -3,6 +3,7 @@
 // kernel launches.  Every arithmetic step of the method runs in the CUDA
 // kernels; this file only moves pointers and sizes around.
 #include <algorithm>
+#include <climits>
 #include <cmath>
 #include <cstring>
 #include <new>
@@ -333,6 +334,38 @@ void choose_splits(const rq_cache *c, int T, int units, int which, int *S, int *
     *chunk = best_ch;
 }
 
+// The splits of a windowed call over the two runs of tokens it reads (the
+// sinks', the window's): the chunk size with the least wave-quantised work, by
+// choose_splits' cost.  Where that needs more splits than the workspace has
+// slots for (nearly the whole of the largest sequences visible), the whole
+// sequence is dealt out and what lies between the runs is masked.
+void choose_window_splits(const rq_cache *c, int units, int which, DecodeArgs *a) {
+    int tw = 0, ts = 0;
+    for (int b = 0; b < a->B; b++) {
+        const WindowRuns r = window_runs(a->seqT.v[b], a->n_tail, a->window, a->sinks);
+        tw = std::max(tw, a->seqT.v[b] - r.w_tile);
+        ts = std::max(ts, r.sink_end);
+    }
+    const int nw = (tw + kTokTile - 1) / kTokTile, ns = (ts + kTokTile - 1) / kTokTile;
+    long best = -1;
+    for (int ch = 1; ch <= kMaxChunk / kTokTile; ch++) {
+        const int s_sink = (ns + ch - 1) / ch, S = s_sink + (nw + ch - 1) / ch;
+        if (S > c->lay.splits_max) continue;
+        const long slots = std::max(1, c->occ[which][ch - 1] * c->sms);
+        const long cost = ((long)S * units + slots - 1) / slots * (ch + RQ_SPLIT_OVERHEAD_TILES);
+        if (best < 0 || cost < best) {
+            best = cost;
+            a->S = S;
+            a->s_sink = s_sink;
+            a->chunk = ch * kTokTile;
+        }
+    }
+    if (best < 0) {
+        a->s_sink = 0;
+        choose_splits(c, a->T, units, which, &a->S, &a->chunk);
+    }
+}
+
 }  // namespace
 
 namespace rq {
@@ -648,10 +681,21 @@ int rq_append(rq_cache *c, int layer, int loop, const void *k, const void *v, in
 // workspace (partial stride splits_max).  Otherwise in the caller's scratch
 // (stride = the split count this call uses).
 // app_k != nullptr: append app_n tokens to the loop first (rq_append_decode_attn).
+// win != nullptr: a windowed call (`out` then points to elements of win->out_type).
+struct WindowSpec {
+    int window, sinks, out_type;
+};
+// The arguments of the windowed calls as the caller gave them; window 0
+// (every token visible) becomes a window no sequence reaches.
+static bool window_spec(int window, int sinks, int out_type, WindowSpec *w) {
+    if (window < 0 || sinks < 0 || (out_type != RQ_OUT_FP32 && out_type != RQ_OUT_BF16)) return false;
+    *w = WindowSpec{window > 0 ? window : INT_MAX, window > 0 ? sinks : 0, out_type};
+    return true;
+}
 static int decode_common(rq_cache *c, int layer, int loop, const void *q, float *out, float scale,
                          void *stream, bool bf16, float *partials = nullptr, size_t partial_floats = 0,
                          int *counters = nullptr, size_t max_units = 0, const void *app_k = nullptr,
-                         const void *app_v = nullptr, int app_n = 0) {
+                         const void *app_v = nullptr, int app_n = 0, const WindowSpec *win = nullptr) {
     if (!c || !q || !out) return RQ_ERR_INVALID;
     if (!on_cache_device(c)) return RQ_ERR_INVALID;
     const Layout &L = c->lay;
@@ -719,7 +763,17 @@ static int decode_common(rq_cache *c, int layer, int loop, const void *q, float 
         }
     }
     const int units = a.B * a.H * (a.G > 2 ? a.G / 2 : 1);
-    choose_splits(c, a.T, units, bf16 ? 0 : a.nr, &a.S, &a.chunk);
+    if (win) {
+        a.window = win->window;
+        a.sinks = win->sinks;
+        if (win->out_type == RQ_OUT_BF16) {
+            a.out16 = (uint16_t *)out;
+            a.out = nullptr;
+        }
+        choose_window_splits(c, units, bf16 ? 0 : a.nr, &a);
+    } else {
+        choose_splits(c, a.T, units, bf16 ? 0 : a.nr, &a.S, &a.chunk);
+    }
     if (partials) {
         a.splits_max = std::max(a.S, 1);
         if ((size_t)a.B * a.Hq * a.splits_max * kPartialStride > partial_floats) return RQ_ERR_CAPACITY;
@@ -749,6 +803,9 @@ static int decode_common(rq_cache *c, int layer, int loop, const void *q, float 
         if (s == RQ_OK) nt += app_n;
         return s;
     }
+    if (win && a.S > 0)   // the windowed kernels merge their splits themselves
+        return cuda_status(bf16 ? launch_decode_bf16(a, st)
+                                : launch_decode_rq_window(a, cfg.anchor_bits, cfg.resid_bits, st));
     if (!bf16 && a.S > 0)   // the decode kernel merges its splits and the tail itself
         return cuda_status(launch_decode_rq(a, cfg.anchor_bits, cfg.resid_bits, st));
     if (bf16 && a.S > 0) {
@@ -759,7 +816,10 @@ static int decode_common(rq_cache *c, int layer, int loop, const void *q, float 
     std::memset(&cb, 0, sizeof(cb));
     cb.partials = a.partials;
     cb.q = a.q;
-    cb.out = out;
+    cb.out = a.out;
+    cb.out16 = a.out16;
+    cb.window = a.window;
+    cb.sinks = a.sinks;
     cb.tail_k = a.tail_k;
     cb.tail_v = a.tail_v;
     cb.B = a.B;
@@ -803,6 +863,14 @@ int rq_append_decode_attn(rq_cache *c, int layer, int loop, const void *k, const
 int rq_decode_attn_bf16(rq_cache *c, int layer, int loop, const void *q, float *out, float scale,
                         void *stream) {
     return decode_common(c, layer, loop, q, out, scale, stream, true);
+}
+
+int rq_decode_attn_window(rq_cache *c, int layer, int loop, const void *q, void *out, int out_type, float scale,
+                          int window, int sinks, void *stream) {
+    WindowSpec w;
+    if (!c || !window_spec(window, sinks, out_type, &w)) return RQ_ERR_INVALID;
+    return decode_common(c, layer, loop, q, (float *)out, scale, stream, c->lay.cfg.format == RQ_FMT_BF16, nullptr, 0,
+                         nullptr, 0, nullptr, nullptr, 0, &w);
 }
 
 int rq_prefill_attn(rq_cache *c, int layer, int loop, const void *q, int n, float *out, float scale,

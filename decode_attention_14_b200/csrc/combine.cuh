@@ -52,10 +52,13 @@ __device__ __forceinline__ void merge_partials(const float *part, int S, int tid
 
 // Run by 128 threads (thread `tid` owns element tid of the row).  `sync` is a
 // barrier over exactly those threads; `red` is 4 floats of shared memory.
+// Tail tokens [hole.first, hole.last) are masked; the row goes to out_row, or
+// as BF16 to out16 where that is given.
 template <typename Sync>
 __device__ __forceinline__ void combine_row(const float *part, int S, const uint16_t *q_row, float scale_log2,
                                             const uint16_t *tail_k, const uint16_t *tail_v, size_t tail_stride,
-                                            int n_tail, float *out_row, int tid, float *red, Sync sync) {
+                                            int n_tail, float *out_row, int tid, float *red, Sync sync,
+                                            TailMask hole = TailMask{0, 0}, uint16_t *out16 = nullptr) {
     const int lane = tid & 31, warp = tid >> 5;
     // q and the first tail token are fetched first, so that their latency
     // overlaps the partials' (L2 loads: the tail rows may have been written
@@ -70,6 +73,7 @@ __device__ __forceinline__ void combine_row(const float *part, int S, const uint
     merge_partials(part, S, tid, M, l, o);
     // tail tokens, folded in one by one with the running-max rule
     for (int j = 0; j < n_tail; j++) {
+        if (j >= hole.first && j < hole.last) continue;   // uniform
         const size_t row = (size_t)j * tail_stride;
         const float kj = j == 0 ? k0 : bf16_to_f32(__ldcg(tail_k + row + tid));
         const float vj = j == 0 ? v0 : bf16_to_f32(__ldcg(tail_v + row + tid));
@@ -85,7 +89,9 @@ __device__ __forceinline__ void combine_row(const float *part, int S, const uint
         l = l * c0 + c1;
         M = nm;
     }
-    out_row[tid] = (l > 0.f) ? o / l : 0.f;
+    const float x = (l > 0.f) ? o / l : 0.f;
+    if (out16) out16[tid] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
+    else out_row[tid] = x;
 }
 
 }  // namespace rq

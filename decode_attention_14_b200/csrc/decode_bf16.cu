@@ -7,6 +7,11 @@
 // (sequence, kv head); pass 1 writes the chunk's logits, pass 2 sums
 // exp2(z - chunk max) * v; the combine kernel merges the partials and the
 // BF16 tail tokens.
+//
+// WIN (rq_decode_attn_window): the sinks' and the window's tokens are dealt
+// over splits of their own (window_split), what lies between them is masked,
+// and the last CTA of a (sequence, kv head, head pair) to arrive merges the
+// splits itself: one launch, which is what a short window costs.
 #include <math_constants.h>
 
 #include "combine.cuh"
@@ -27,7 +32,11 @@ __device__ __forceinline__ void load16_bf16(const uint16_t *p, float v[16]) {
     }
 }
 
-template <int GK>
+struct BlockSync {
+    __device__ __forceinline__ void operator()() const { __syncthreads(); }
+};
+
+template <int GK, bool WIN>
 __global__ void __launch_bounds__(128) decode_bf16_kernel(const DecodeArgs a) {
     extern __shared__ float s_scores[];   // [GK][chunk]
     __shared__ float s_q[GK][kHeadDim];
@@ -40,8 +49,9 @@ __global__ void __launch_bounds__(128) decode_bf16_kernel(const DecodeArgs a) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, sub = lane >> 3, seg = lane & 7;
     const int hq0 = h * a.G + pair * GK;
     const int Tb = a.seqT.v[b];   // this sequence's committed tokens
-    int t0, n;
-    split_range(split, a.S, Tb, &t0, &n);
+    int t0, n, m0 = 0, m1 = 0;    // WIN: the split's tokens [m0, m1) are masked
+    if (WIN) window_split(split, a.s_sink, a.S, Tb, 0, a.window, a.sinks, &t0, &n, &m0, &m1);
+    else split_range(split, a.S, Tb, &t0, &n);
     const size_t bh = (size_t)b * a.H + h;
 
 #pragma unroll
@@ -59,7 +69,7 @@ __global__ void __launch_bounds__(128) decode_bf16_kernel(const DecodeArgs a) {
     for (int gq = 0; gq < GK; gq++) mloc[gq] = -CUDART_INF_F;
     for (int it = warp * 4; it < n; it += 16) {
         const int tl = it + sub;
-        const bool valid = tl < n;
+        const bool valid = tl < n && !(WIN && tl >= m0 && tl < m1);
         const size_t rec = bh * a.Tp + (size_t)min(t0 + tl, Tb - 1);
         float k[16];
         load16_bf16(a.bf[0] + rec * kHeadDim + seg * 16, k);
@@ -98,10 +108,14 @@ __global__ void __launch_bounds__(128) decode_bf16_kernel(const DecodeArgs a) {
     }
     for (int it = warp * 4; it < n; it += 16) {
         const int tl = it + sub;
-        const bool valid = tl < n;
+        const bool valid = tl < n && !(WIN && tl >= m0 && tl < m1);
         const size_t rec = bh * a.Tp + (size_t)min(t0 + tl, Tb - 1);
         float v[16];
         load16_bf16(a.bf[1] + rec * kHeadDim + seg * 16, v);
+        if (WIN && !valid) {   // whatever a masked token holds, nothing of it times weight 0
+#pragma unroll
+            for (int i = 0; i < 16; i++) v[i] = 0.f;
+        }
 #pragma unroll
         for (int gq = 0; gq < GK; gq++) {
             const float p = valid ? exp2f(s_scores[gq * a.chunk + tl] - M[gq]) : 0.f;
@@ -134,11 +148,25 @@ __global__ void __launch_bounds__(128) decode_bf16_kernel(const DecodeArgs a) {
             part[kHeadDim + 1] = s_lsum[0][gq] + s_lsum[1][gq] + s_lsum[2][gq] + s_lsum[3][gq];
         }
     }
+    if (WIN) {
+        __shared__ int s_last;
+        __threadfence();
+        __syncthreads();
+        const int unit = (b * a.H + h) * npairs + pair;
+        if (tid == 0) s_last = (atomicAdd(&a.counters[unit], 1) == a.S - 1);
+        __syncthreads();
+        if (!s_last) return;
+        __threadfence();
+        if (tid == 0) a.counters[unit] = 0;   // ready for the next call
+#pragma unroll 1
+        for (int gq = 0; gq < GK; gq++) {
+            const size_t row = (size_t)b * a.Hq + hq0 + gq;
+            combine_row(a.partials + row * a.splits_max * kPartialStride, a.S, a.q + row * kHeadDim, a.scale_log2,
+                        nullptr, nullptr, 0, 0, a.out16 ? nullptr : a.out + row * kHeadDim, tid, &s_red[0][0],
+                        BlockSync(), TailMask{0, 0}, a.out16 ? a.out16 + row * kHeadDim : nullptr);
+        }
+    }
 }
-
-struct BlockSync {
-    __device__ __forceinline__ void operator()() const { __syncthreads(); }
-};
 
 // One CTA per (sequence, query head): merges the split partials and the BF16
 // tail tokens (combine_row) and writes o / l (zero when nothing was attended).
@@ -150,17 +178,23 @@ __global__ void __launch_bounds__(128) combine_kernel(const CombineArgs a) {
     const size_t trow = ((size_t)b * a.tail_cap * a.H + h) * kHeadDim;
     combine_row(a.partials + row * a.splits_max * kPartialStride, a.S, a.q + row * kHeadDim, a.scale_log2,
                 a.tail_k ? a.tail_k + trow : nullptr, a.tail_v ? a.tail_v + trow : nullptr, (size_t)a.H * kHeadDim,
-                a.n_tail, a.out + row * kHeadDim, tid, s_red, BlockSync());
+                a.n_tail, a.out16 ? nullptr : a.out + row * kHeadDim, tid, s_red, BlockSync(),
+                a.window > 0 ? tail_mask(0, a.n_tail, a.window, a.sinks) : TailMask{0, 0},
+                a.out16 ? a.out16 + row * kHeadDim : nullptr);
 }
 
 }  // namespace
 
 cudaError_t launch_decode_bf16(const DecodeArgs &a, cudaStream_t st) {
     const size_t smem_g1 = (size_t)a.chunk * sizeof(float);
-    if (a.G == 1) {
-        decode_bf16_kernel<1><<<dim3(a.S, a.H, a.B), 128, smem_g1, st>>>(a);
+    const dim3 grid(a.S, a.H, a.G == 1 ? a.B : a.B * (a.G / 2));
+    if (a.window > 0) {
+        if (a.G == 1) decode_bf16_kernel<1, true><<<grid, 128, smem_g1, st>>>(a);
+        else decode_bf16_kernel<2, true><<<grid, 128, 2 * smem_g1, st>>>(a);
+    } else if (a.G == 1) {
+        decode_bf16_kernel<1, false><<<grid, 128, smem_g1, st>>>(a);
     } else {
-        decode_bf16_kernel<2><<<dim3(a.S, a.H, a.B * (a.G / 2)), 128, 2 * smem_g1, st>>>(a);
+        decode_bf16_kernel<2, false><<<grid, 128, 2 * smem_g1, st>>>(a);
     }
     return cudaGetLastError();
 }
@@ -168,8 +202,9 @@ cudaError_t launch_decode_bf16(const DecodeArgs &a, cudaStream_t st) {
 int decode_bf16_occupancy(int G, int chunk) {
     int n = 0;
     const size_t smem = (size_t)chunk * sizeof(float) * (G == 1 ? 1 : 2);
-    cudaError_t e = G == 1 ? cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_bf16_kernel<1>, 128, smem)
-                           : cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_bf16_kernel<2>, 128, smem);
+    cudaError_t e =
+        G == 1 ? cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_bf16_kernel<1, false>, 128, smem)
+               : cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_bf16_kernel<2, false>, 128, smem);
     return (e == cudaSuccess && n > 0) ? n : 1;
 }
 

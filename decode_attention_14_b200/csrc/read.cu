@@ -48,7 +48,7 @@ constexpr int kWarps = 4;                          // warps per CTA
 static_assert(32 * kWarps == kHeadDim, "a thread per sign");
 constexpr int kRecs = 16;                          // records of a tile
 #ifndef RQ_READ_TILES
-#define RQ_READ_TILES 2
+#define RQ_READ_TILES 4
 #endif
 #ifndef RQ_READ_SLOTS
 #define RQ_READ_SLOTS 4
@@ -464,9 +464,11 @@ cudaError_t launch_bits(const ReadArgs &a, unsigned blocks, cudaStream_t st) {
 cudaError_t launch_read(const ReadArgs &args, int ba, int br, cudaStream_t st) {
     ReadArgs a = args;
     const long long units = 2LL * a.B * a.H, nt = tiles_of(a.t0, a.n);
-    // two tiles a warp share its set-up and overlap; one while that leaves
-    // fewer warps than the 148 SMs hold (16 each)
-    a.tiles = units * nt <= 148 * 16 * 2 ? 1 : kTiles;
+    // tiles of one warp share its set-up and overlap, as long as four rounds of
+    // the 16 warps an SM holds remain to even out the end: at 8k b4 (residual)
+    // 99 / 104 / 119 us with 4 / 2 / 1, at 15 000 tiles 24.4 / 21.1 / 21.2 us
+    a.tiles = kTiles;
+    while (a.tiles > 1 && units * nt < 148LL * 16 * 4 * a.tiles) a.tiles /= 2;
     const int per = a.tiles * kWarps;
     const long long blocks = units * ((nt + per - 1) / per);
     if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;

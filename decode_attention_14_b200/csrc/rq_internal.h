@@ -188,6 +188,12 @@ struct DecodeArgs {
     float scale_log2;         // softmax_scale * log2(e)
     int rotate;
     uint32_t sigma[4];
+    // windowed calls: the query sees positions p >= P - window (P: committed
+    // and tail tokens of its sequence) and p < sinks; the first s_sink of the
+    // S splits deal out the sinks' tiles, the others the window's.  out16: the
+    // output in BF16 instead of `out`
+    int window, sinks, s_sink;
+    uint16_t *out16;
 };
 
 // Tokens [*t0, *t0 + *n) of split `split` of S: the ceil(T/64) tiles are
@@ -199,6 +205,47 @@ __host__ __device__ inline void split_range(int split, int S, int T, int *t0, in
     *n = (hi * kTokTile < T ? hi * kTokTile : T) - *t0;
 }
 
+// The two runs of committed tokens that a windowed query sees of a sequence of
+// T committed and n_tail tail tokens: [0, sink_end) and [w_tile, T), the
+// latter from a tile boundary on, with tokens of [sinks, w0) masked.
+struct WindowRuns {
+    int sink_end, w_tile, w0;
+};
+__host__ __device__ inline WindowRuns window_runs(int T, int n_tail, int window, int sinks) {
+    WindowRuns r;
+    const long long first = (long long)T + n_tail - window;   // of the window
+    r.w0 = first > T ? T : first > 0 ? (int)first : 0;
+    r.w_tile = r.w0 == T ? T : r.w0 / kTokTile * kTokTile;     // no window token committed: no window run
+    r.sink_end = sinks < r.w_tile ? sinks : r.w_tile;
+    return r;
+}
+// The tokens [*t0, *t0 + *n) of split `split` of S, the first s_sink of them
+// splits of the sinks' run, and of them the masked ones [*m0, *m1) (relative
+// to *t0).  s_sink = 0 with a sinks' run somewhere: the whole sequence is dealt
+// out, what lies between the runs masked.
+__host__ __device__ inline void window_split(int split, int s_sink, int S, int T, int n_tail, int window, int sinks,
+                                             int *t0, int *n, int *m0, int *m1) {
+    const WindowRuns r = window_runs(T, n_tail, window, sinks);
+    if (split < s_sink) {
+        split_range(split, s_sink, r.sink_end, t0, n);
+        *m0 = *m1 = 0;
+        return;
+    }
+    const int from = s_sink > 0 || r.sink_end == 0 ? r.w_tile : 0;
+    split_range(split - s_sink, S - s_sink, T - from, t0, n);
+    *t0 += from;
+    *m0 = sinks > *t0 ? sinks - *t0 : 0;
+    *m1 = r.w0 - *t0;
+}
+
+// Tail tokens [first, last) that the query does not see.
+struct TailMask {
+    int first, last;
+};
+__host__ __device__ inline TailMask tail_mask(int T, int n_tail, int window, int sinks) {
+    return TailMask{sinks > T ? sinks - T : 0, window < n_tail ? n_tail - window : 0};
+}
+
 struct CombineArgs {
     const float *partials;
     const uint16_t *q;
@@ -206,6 +253,8 @@ struct CombineArgs {
     float *out;               // [B][Hq][d]
     int B, H, Hq, G, S, splits_max, n_tail, tail_cap;
     float scale_log2;
+    int window, sinks;        // a windowed call's (window 0: none); every sequence then holds no committed token
+    uint16_t *out16;          // the output in BF16 instead of `out`, or null
 };
 
 // Block-table writes and whole-block copies of a paged cache (copy-on-write
@@ -233,6 +282,8 @@ cudaError_t launch_bf16_store(const Bf16StoreArgs &a, cudaStream_t st);
 // a.nr residual records: 0, 1, or (INT4 anchor / INT2 residuals only) 2-3
 bool decode_rq_supported(int ba, int br, int nr);
 cudaError_t launch_decode_rq(const DecodeArgs &a, int ba, int br, cudaStream_t st);
+cudaError_t launch_decode_rq_window(const DecodeArgs &a, int ba, int br, cudaStream_t st);
+// a.window > 0: windowed, the splits merged in the same launch
 cudaError_t launch_decode_bf16(const DecodeArgs &a, cudaStream_t st);
 cudaError_t launch_combine(const CombineArgs &a, cudaStream_t st);
 // resident CTAs per SM of the decode kernels for a given chunk (tokens per CTA)

@@ -270,6 +270,31 @@ int rq_prefill_attn(rq_cache *cache, int layer, int loop, const void *q_bf16, in
                     float softmax_scale, void *stream);
 
 /*
+ * Single-token decode attention with a sliding window and sinks, over either
+ * cache format: of the tokens that rq_decode_attn (RQ_FMT_BF16:
+ * rq_decode_attn_bf16) sees, at positions 0 .. P - 1 of each sequence
+ * (committed tokens, then the loop's tail), the query -- the token at P - 1 --
+ * attends to the last `window` ones and to the first `sinks` ones.  The
+ * abstract's method changes nothing about attention itself; this is the
+ * sliding-window form of it that long-context models use.
+ *   window: > 0; 0 for no window (every token; sinks is then ignored).  A
+ *     window longer than the sequence is the whole sequence.
+ *   sinks:  >= 0; may reach into the window.
+ *   q_bf16: device, [batch][num_q_heads][head_dim] BF16.
+ *   out:    device, [batch][num_q_heads][head_dim] of out_type (rq_out_type).
+ *   softmax_scale: as for rq_decode_attn.
+ * Only the records of visible tokens (in whole 64-token tiles) are read;
+ * masked tokens do not enter the result, whatever they hold.  With no token
+ * at all the output is zero.  fp32 results are more precise than
+ * rq_decode_attn's (28-bit instead of 22-bit value weights).  Overlap,
+ * workspace and stream rules are rq_decode_attn's.
+ * Errors: INVALID (null pointer, index, window < 0, sinks < 0, out_type),
+ * UNSUPPORTED (as rq_decode_attn), CUDA.
+ */
+int rq_decode_attn_window(rq_cache *cache, int layer, int loop, const void *q_bf16, void *out, int out_type,
+                          float softmax_scale, int window, int sinks, void *stream);
+
+/*
  * rq_decode_attn without any allocation: identical arguments, results and
  * errors, except that the split-combine partials go to a fixed array the
  * library holds in device memory (8 MiB per GPU that loads the library, kept

@@ -1,0 +1,283 @@
+"""Sliding-window attention with sinks (rq_decode_attn_window,
+rq_prefill_attn_window) against a plain fp64 softmax over the keys and values
+that the cache holds (rq_cache_export through the oracle's reconstruction, or
+the stored BF16 values, then the BF16 tail).
+
+Tolerances, fp32 output.  Decode of the compressed cache: value weights in 28
+bits and q in 24 bits of fixed point relative to their largest, sums in int32:
+the weight error of a token is at most 2^-29 of the bound max|s| max(scale),
+times a code of at most 15, random over the tokens; the logit error at most
+2^-22 max|q| times |k|_1.  With |k|_1 below 128 * 3 (10 in 4 channels) and
+max|q| about 4, scaled by 1/sqrt(128): about 4e-5 at the very worst, and the
+output moves by at most twice that times the values' spread: 2e-4 max abs and
+2e-5 relative L2 leave a margin for fp32 sums.  The chunk kernel splits
+probabilities and rotated queries into BF16 pairs (relative 2^-17 each): the
+contract's 1e-3 / 2e-3.  BF16 caches: fp32 products and sums (decode), or
+probabilities as BF16 pairs.  BF16 output adds half a step, 2^-8 |x|.
+"""
+import numpy as np
+import pytest
+import torch
+
+import decode_attention_14_b200 as rq
+import synth
+from oracle import oracle as orc
+
+import rqharness as H
+
+pytestmark = pytest.mark.gpu
+BIG = 1 << 30
+
+
+def keys_values(bt, layer, loop, lens):
+    """Per sequence [2][H][len + n_tail][d] fp64: what (layer, loop) sees."""
+    cfg = bt.cfg
+    Lg, B, Hk = cfg.loops_per_group, cfg.batch, cfg.num_kv_heads
+    if cfg.format == rq.RQ_FMT_BF16:
+        X = bt.inputs[(layer, loop // Lg)]
+        x = [orc.bf16_bits_to_f64(synth.bf16_to_u16(X[kv][loop % Lg])) for kv in range(2)]
+        return [np.stack([x[kv][b, :lens[b]].transpose(1, 0, 2) for kv in range(2)]) for b in range(B)]
+    grp, j = loop // Lg, loop % Lg
+    rec = [H.reconstruct_gpu(bt, layer, grp, kv).reshape(Lg, B, Hk, -1, 128)[j] for kv in range(2)]
+    out = [np.stack([rec[kv][b, :, :lens[b]] for kv in range(2)]) for b in range(B)]
+    if j != Lg - 1 and bt.n_tail:
+        X = bt.inputs[(layer, grp)]
+        for b in range(B):
+            tail = np.stack([orc.bf16_bits_to_f64(synth.bf16_to_u16(X[kv][j][b:b + 1, bt.T:]))[0].transpose(1, 0, 2)
+                             for kv in range(2)])
+            out[b] = np.concatenate([out[b], tail], 2)
+    return out
+
+
+def reference(kv, q, window, sinks):
+    """q [B][n][Hq][d] -> the same in fp64; each of the last n positions sees its window and the sinks."""
+    qf = q.double().cpu().numpy()
+    B, n, Hq, _ = qf.shape
+    out = np.zeros_like(qf)
+    for b in range(B):
+        k, v = kv[b]
+        Hk, P = k.shape[0], k.shape[1]
+        if P == 0:
+            continue
+        pos = np.arange(P - n, P)[:, None]
+        t = np.arange(P)[None, :]
+        seen = (t <= pos) & ((t > pos - window) | (t < sinks)) if window else t <= pos
+        for h in range(Hq):
+            z = qf[b, :, h] @ k[h * Hk // Hq].T / np.sqrt(128.0)
+            z = np.where(seen, z, -np.inf)
+            p = np.exp(z - z.max(1, keepdims=True))
+            vv = np.where(seen.any(0)[:, None], v[h * Hk // Hq], 0.0)
+            out[b, :, h] = (p / p.sum(1, keepdims=True)) @ vv
+    return out
+
+
+def check(out, ref, rel, mx):
+    g = out.double().cpu().numpy().reshape(ref.shape)
+    half = 2.0 ** -8 if out.dtype == torch.bfloat16 else 0.0
+    far = np.maximum(np.abs(g - ref) - half * np.abs(ref), 0.0)
+    assert np.isfinite(g).all()
+    assert np.linalg.norm(far) <= rel * max(np.linalg.norm(ref), 1e-300) and far.max() <= mx, (
+        np.linalg.norm(far) / max(np.linalg.norm(ref), 1e-300), far.max())
+
+
+def queries(seed, *shape):
+    return torch.randn(shape, device="cuda", generator=torch.Generator("cuda").manual_seed(seed)).bfloat16()
+
+
+WINDOWS = [(1, 0), (1, 1), (2, 0), (63, 4), (64, 4), (65, 0), (100, 70), (128, 64), (150, 200), (0, 0), (0, 9),
+           (BIG, 0), (BIG, 5)]
+
+
+@pytest.mark.parametrize("T,n_tail", [(1, 0), (1, 1), (64, 1), (65, 3), (200, 0), (333, 2), (1000, 5)])
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+def test_decode_windows(T, n_tail, out):
+    bt = H.build(T=T, n_tail=n_tail, H=2, Hq=4, seed=0x5EEDBB01)
+    q = queries(1, 1, 4, 128)
+    for loop in (0, 3):
+        kv = keys_values(bt, 0, loop, [T])
+        for window, sinks in WINDOWS:
+            ref = reference(kv, q[:, None], window, sinks)[:, 0]
+            check(bt.cache.decode_window(0, loop, q, window, sinks, dtype=out), ref, 2e-5, 2e-4)
+    bt.cache.check()
+    bt.cache.close()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(g=32), dict(ba=2), dict(br=4, g=32), dict(ba=2, br=4), dict(rotate=False), dict(Hq=2), dict(Hq=8), dict(Hq=16),
+    dict(loops=2, Lg=1), dict(anchor_mode=rq.ANCHOR_CHAINED), dict(layers=2, rotation_per_layer=True),
+    dict(B=3, block_tokens=128, num_blocks=24, prepare=lambda c: c.shuffle_free_blocks(5)),
+    dict(B=3, block_tokens=256, num_blocks=12, prepare=lambda c: c.shuffle_free_blocks(5), Hq=8),
+], ids=lambda kw: "-".join(f"{k}{v}" for k, v in kw.items() if k != "prepare"))
+def test_decode_window_variants(kw):
+    bt = H.build(**{"T": 700, "n_tail": 2, "H": 2, "Hq": 4, "seed": 0x5EEDBB02, **kw})
+    cfg = bt.cfg
+    q = queries(2, cfg.batch, cfg.num_q_heads, 128)
+    layer = cfg.num_layers - 1
+    for loop in range(cfg.num_loops):
+        kv = keys_values(bt, layer, loop, [700] * cfg.batch)
+        for window, sinks in ((300, 4), (64, 130), (257, 0)):
+            ref = reference(kv, q[:, None], window, sinks)[:, 0]
+            check(bt.cache.decode_window(layer, loop, q, window, sinks), ref, 2e-5, 2e-4)
+    bt.cache.check()
+    bt.cache.close()
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_decode_windows_of_ragged_sequences(paged):
+    """Sequences of different lengths, one empty: each has a window of its own; with no token at all the output is zero."""
+    kw = dict(block_tokens=128, num_blocks=48, prepare=lambda c: c.shuffle_free_blocks(3)) if paged else {}
+    bt = H.build(B=5, T=1100, H=2, Hq=2, seed=0x5EEDBB03, **kw)
+    lens = [1100, 64, 0, 130, 129]
+    for b in range(5):
+        bt.cache.truncate_seq(0, 0, b, lens[b])
+    K, V = bt.inputs[(0, 0)]
+    q = queries(3, 5, 2, 128)
+
+    def sweep(loop):
+        kv = keys_values(bt, 0, loop, lens)
+        for window, sinks in ((1, 0), (2, 1), (3, 0), (64, 4), (66, 200), (500, 64), (1030, 64), (1024, 0)):
+            ref = reference(kv, q[:, None], window, sinks)[:, 0]
+            check(bt.cache.decode_window(0, loop, q, window, sinks), ref, 2e-5, 2e-4)
+
+    sweep(3)
+    sweep(1)
+    tail = torch.randn((2, 5, 3, 2, 128), device="cuda", generator=torch.Generator("cuda").manual_seed(1)).bfloat16()
+    bt.cache.append(0, 1, tail[0].contiguous(), tail[1].contiguous())
+    bt.inputs[(0, 0)] = tuple([torch.cat((X[j], tail[i]), 1) for j in range(4)] for i, X in ((0, K), (1, V)))
+    bt.n_tail = 3
+    sweep(1)
+    bt.cache.check()
+    bt.cache.close()
+
+
+def test_decode_window_of_an_empty_cache():
+    """Nothing committed: the tail alone, windows shorter than it; and nothing at all."""
+    bt = H.build(T=0, n_tail=6, B=2, H=2, Hq=4, max_tokens=64, seed=0x5EEDBB04)
+    q = queries(4, 2, 4, 128)
+    for dtype in (torch.float32, torch.bfloat16):
+        for window, sinks in ((1, 0), (2, 1), (3, 2), (6, 0), (0, 0), (4, 9)):
+            kv = [
+                np.stack([orc.bf16_bits_to_f64(synth.bf16_to_u16(bt.inputs[(0, 0)][i][0][b:b + 1]))[0].transpose(1, 0, 2)
+                          for i in range(2)]) for b in range(2)]
+            ref = reference(kv, q[:, None], window, sinks)[:, 0]
+            check(bt.cache.decode_window(0, 0, q, window, sinks, dtype=dtype), ref, 2e-5, 2e-4)
+        assert (bt.cache.decode_window(0, 3, q, 5, 1, dtype=dtype) == 0).all()
+    bt.cache.close()
+
+
+@pytest.mark.parametrize("Hq", [2, 4, 16])
+def test_decode_windows_of_a_bf16_cache(Hq):
+    bt = H.build(loops=1, Lg=1, B=3, T=1300, H=2, Hq=Hq, fmt=rq.RQ_FMT_BF16, seed=0x5EEDBB05)
+    lens = [1300, 77, 0]
+    for b in range(3):
+        bt.cache.truncate_seq(0, 0, b, lens[b])
+    q = queries(5, 3, Hq, 128)
+    kv = keys_values(bt, 0, 0, lens)
+    for dtype in (torch.float32, torch.bfloat16):
+        for window, sinks in WINDOWS + [(1234, 64), (700, 600)]:
+            ref = reference(kv, q[:, None], window, sinks)[:, 0]
+            check(bt.cache.decode_window(0, 0, q, window, sinks, dtype=dtype), ref, 4e-6, 4e-5)
+    bt.cache.check()
+    bt.cache.close()
+
+
+def _poison(bt, layer, loop, where, value, chunk=64):
+    """The group's K and V with `value` in whole rows of the tokens `where`, appended again."""
+    K, V = ([x.clone() for x in X] for X in bt.inputs[(layer, 0)])
+    for X in (K, V):
+        for x in X:
+            x[:, where] = value
+    bt.cache.truncate(layer, 0, 0)
+    bt.recon.clear()
+    H.fill_group(bt, layer, 0, K, V, chunk)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf"), 3e38])
+@pytest.mark.parametrize("fmt", [rq.RQ_FMT_RESIDUAL, rq.RQ_FMT_BF16])
+def test_decode_does_not_see_what_masked_tokens_hold(fmt, value):
+    """NaN, infinities and the largest numbers in every token outside the window and the sinks, in K and V."""
+    Lg = 4 if fmt == rq.RQ_FMT_RESIDUAL else 1
+    bt = H.build(loops=Lg, Lg=Lg, T=300, H=2, Hq=4, fmt=fmt, seed=0x5EEDBB06, max_tokens=320)
+    q = queries(6, 1, 4, 128)
+    window, sinks = 100, 5
+    ref = {loop: reference(keys_values(bt, 0, loop, [300]), q[:, None], window, sinks)[:, 0] for loop in range(Lg)}
+    _poison(bt, 0, 0, slice(5, 200), value)
+    for loop in range(Lg):
+        check(bt.cache.decode_window(0, loop, q, window, sinks), ref[loop], 2e-5, 2e-4)
+    bt.cache.close()
+
+
+def test_decode_window_equals_itself_in_any_order_of_calls():
+    """Bit-equal on repetition, on a side stream, in a replayed graph and between other calls on the cache; a window
+    longer than the sequence agrees with rq_decode_attn to that call's precision."""
+    bt = H.build(B=2, T=900, H=2, Hq=4, n_tail=1, seed=0x5EEDBB07)
+    q = queries(7, 2, 4, 128)
+    first = bt.cache.decode_window(0, 1, q, 333, 4)
+    full = bt.cache.decode_window(0, 1, q, 0)
+    ref = reference(keys_values(bt, 0, 1, [900, 900]), q[:, None], 0, 0)[:, 0]
+    rel = lambda x: np.linalg.norm(x.double().cpu().numpy() - ref) / np.linalg.norm(ref)   # noqa: E731
+    assert rel(full) <= 2e-5 and rel(bt.cache.decode(0, 1, q)) <= 1e-3
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out = torch.zeros_like(first)
+    bt.cache.decode_window(0, 1, q, 333, 4, out=out, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(out, first)
+    g = torch.cuda.CUDAGraph()
+    out2 = torch.zeros_like(first)
+    with torch.cuda.graph(g):
+        bt.cache.decode_window(0, 2, q, 50, 0)
+        bt.cache.decode_window(0, 1, q, 333, 4, out=out2)
+    for _ in range(3):
+        out2.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out2, first)
+        bt.cache.decode(0, 1, q)
+        assert torch.equal(bt.cache.decode_window(0, 1, q, 333, 4), first)
+    bt.cache.check()
+    bt.cache.close()
+
+
+def test_a_decode_loop_with_a_window():
+    """Token by token, as a serving loop runs: append, then decode with a window, every loop of the group."""
+    bt = H.build(T=130, H=2, Hq=2, seed=0x5EEDBB08, max_tokens=200)
+    K, V = synth.group_kv(99, 0, 0, 4, (0.1, 0.2, 0.3), 1, 140, 2, device="cuda")
+    bt.cache.truncate(0, 0, 0)
+    bt.T, bt.recon = 130, {}
+    for t0 in range(0, 130, 64):
+        for j in range(4):
+            bt.cache.append(0, j, K[j][:, t0:min(130, t0 + 64)].contiguous(), V[j][:, t0:min(130, t0 + 64)].contiguous())
+    for t in range(130, 136):
+        for j in range(4):
+            q = queries(1000 + 4 * t + j, 1, 2, 128)
+            bt.cache.append(0, j, K[j][:, t:t + 1].contiguous(), V[j][:, t:t + 1].contiguous())
+            got = bt.cache.decode_window(0, j, q, 70, 3)
+            bt.T, bt.n_tail, bt.recon = (t if j < 3 else t + 1), (1 if j < 3 else 0), {}
+            bt.inputs[(0, 0)] = ([k[:, :t + 1] for k in K], [v[:, :t + 1] for v in V])
+            ref = reference(keys_values(bt, 0, j, [bt.T]), q[:, None], 70, 3)[:, 0]
+            check(got, ref, 2e-5, 2e-4)
+    bt.cache.close()
+
+
+def test_window_refusals():
+    bt = H.build(T=20, H=2, Hq=2, seed=0x5EEDBB09)
+    q, out = queries(8, 1, 2, 128), torch.zeros((1, 2, 128), device="cuda")
+
+    def call(layer=0, loop=0, qq=q, oo=out, kind=rq.RQ_OUT_FP32, window=4, sinks=1):
+        return rq.rq_decode_attn_window(bt.cache.h, layer, loop, qq, oo, kind, 0.0, window, sinks)
+
+    assert call() == rq.RQ_OK
+    for kw in (dict(layer=1), dict(layer=-1), dict(loop=4), dict(loop=-1), dict(qq=None), dict(oo=None), dict(kind=2),
+               dict(kind=-1), dict(window=-1), dict(sinks=-1)):
+        assert call(**kw) == rq.RQ_ERR_INVALID, kw
+    for bad in (q.float(), q[:, :1], q[..., ::2]):
+        with pytest.raises(ValueError):
+            bt.cache.decode_window(0, 0, bad, 4)
+    with pytest.raises(ValueError):
+        bt.cache.decode_window(0, 0, q, 4, out=out, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        bt.cache.decode_window(0, 0, q, 4, dtype=torch.float16)
+    with pytest.raises(rq.RQError):
+        bt.cache.decode_window(0, 0, q, -4)
+    bt.cache.close()
