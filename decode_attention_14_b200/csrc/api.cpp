@@ -770,7 +770,16 @@ static int decode_common(rq_cache *c, int layer, int loop, const void *q, float 
             a.out16 = (uint16_t *)out;
             a.out = nullptr;
         }
-        choose_window_splits(c, units, bf16 ? 0 : a.nr, &a);
+        if (bf16) {   // the visible tokens are one run there
+            int run = 0;
+            for (int b = 0; b < a.B; b++) {
+                const long long T = a.seqT.v[b];
+                run = std::max(run, (int)std::min(T, (long long)a.window + a.sinks));
+            }
+            choose_splits(c, run, units, 0, &a.S, &a.chunk);
+        } else {
+            choose_window_splits(c, units, a.nr, &a);
+        }
     } else {
         choose_splits(c, a.T, units, bf16 ? 0 : a.nr, &a.S, &a.chunk);
     }

@@ -18,8 +18,8 @@ namespace rq {
 // (a split with no key has m = -inf: weight 0).  `part` points at slot 0 of
 // the row's partials (stride kPartialStride); it is read with L1-bypassing
 // loads because other CTAs wrote it.
+template <int kBatch = 16>
 __device__ __forceinline__ void merge_partials(const float *part, int S, int tid, float &M, float &l, float &o) {
-    constexpr int kBatch = 16;
     M = -CUDART_INF_F;
     l = 0.f;
     o = 0.f;
@@ -54,7 +54,7 @@ __device__ __forceinline__ void merge_partials(const float *part, int S, int tid
 // barrier over exactly those threads; `red` is 4 floats of shared memory.
 // Tail tokens [hole.first, hole.last) are masked; the row goes to out_row, or
 // as BF16 to out16 where that is given.
-template <typename Sync>
+template <int kBatch = 16, typename Sync>
 __device__ __forceinline__ void combine_row(const float *part, int S, const uint16_t *q_row, float scale_log2,
                                             const uint16_t *tail_k, const uint16_t *tail_v, size_t tail_stride,
                                             int n_tail, float *out_row, int tid, float *red, Sync sync,
@@ -70,7 +70,7 @@ __device__ __forceinline__ void combine_row(const float *part, int S, const uint
         v0 = bf16_to_f32(__ldcg(tail_v + tid));
     }
     float M, l, o;
-    merge_partials(part, S, tid, M, l, o);
+    merge_partials<kBatch>(part, S, tid, M, l, o);
     // tail tokens, folded in one by one with the running-max rule
     for (int j = 0; j < n_tail; j++) {
         if (j >= hole.first && j < hole.last) continue;   // uniform

@@ -8,10 +8,11 @@
 // exp2(z - chunk max) * v; the combine kernel merges the partials and the
 // BF16 tail tokens.
 //
-// WIN (rq_decode_attn_window): the sinks' and the window's tokens are dealt
-// over splits of their own (window_split), what lies between them is masked,
-// and the last CTA of a (sequence, kv head, head pair) to arrive merges the
-// splits itself: one launch, which is what a short window costs.
+// WIN (rq_decode_attn_window): the splits are dealt over the visible tokens
+// only -- the sinks, then the window, as one run with a hole that is stepped
+// over -- so nothing masked is read; and the last CTA of a (sequence, kv head,
+// head pair) to arrive merges the splits itself: one launch, which is what a
+// short window costs.
 #include <math_constants.h>
 
 #include "combine.cuh"
@@ -37,7 +38,7 @@ struct BlockSync {
 };
 
 template <int GK, bool WIN>
-__global__ void __launch_bounds__(128) decode_bf16_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(128, WIN ? (GK == 1 ? 10 : 7) : 0) decode_bf16_kernel(const DecodeArgs a) {
     extern __shared__ float s_scores[];   // [GK][chunk]
     __shared__ float s_q[GK][kHeadDim];
     __shared__ float s_red[4][GK], s_lsum[4][GK];
@@ -49,10 +50,22 @@ __global__ void __launch_bounds__(128) decode_bf16_kernel(const DecodeArgs a) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, sub = lane >> 3, seg = lane & 7;
     const int hq0 = h * a.G + pair * GK;
     const int Tb = a.seqT.v[b];   // this sequence's committed tokens
-    int t0, n, m0 = 0, m1 = 0;    // WIN: the split's tokens [m0, m1) are masked
-    if (WIN) window_split(split, a.s_sink, a.S, Tb, 0, a.window, a.sinks, &t0, &n, &m0, &m1);
-    else split_range(split, a.S, Tb, &t0, &n);
-    const size_t bh = (size_t)b * a.H + h;
+    const size_t bh_row = ((size_t)b * a.H + h) * a.Tp;
+    int t0, n, sink_end = 0, hole = 0;   // WIN: tokens from sink_end on lie `hole` further on
+    if (WIN) {
+        const int w0 = max(0, Tb - a.window);
+        sink_end = min(a.sinks, w0);
+        hole = w0 - sink_end;
+        split_range(split, a.S, Tb - hole, &t0, &n);
+    } else {
+        split_range(split, a.S, Tb, &t0, &n);
+    }
+    // the record of the split's token tl (one past its end repeats the last)
+    auto record = [&](int tl) -> size_t {
+        if (!WIN) return bh_row + (size_t)min(t0 + tl, Tb - 1);
+        const int t = min(t0 + tl, Tb - hole - 1);
+        return bh_row + (size_t)(t >= sink_end ? t + hole : t);
+    };
 
 #pragma unroll
     for (int gq = 0; gq < GK; gq++)
@@ -69,8 +82,8 @@ __global__ void __launch_bounds__(128) decode_bf16_kernel(const DecodeArgs a) {
     for (int gq = 0; gq < GK; gq++) mloc[gq] = -CUDART_INF_F;
     for (int it = warp * 4; it < n; it += 16) {
         const int tl = it + sub;
-        const bool valid = tl < n && !(WIN && tl >= m0 && tl < m1);
-        const size_t rec = bh * a.Tp + (size_t)min(t0 + tl, Tb - 1);
+        const bool valid = tl < n;
+        const size_t rec = record(tl);
         float k[16];
         load16_bf16(a.bf[0] + rec * kHeadDim + seg * 16, k);
 #pragma unroll
@@ -108,14 +121,10 @@ __global__ void __launch_bounds__(128) decode_bf16_kernel(const DecodeArgs a) {
     }
     for (int it = warp * 4; it < n; it += 16) {
         const int tl = it + sub;
-        const bool valid = tl < n && !(WIN && tl >= m0 && tl < m1);
-        const size_t rec = bh * a.Tp + (size_t)min(t0 + tl, Tb - 1);
+        const bool valid = tl < n;
+        const size_t rec = record(tl);
         float v[16];
         load16_bf16(a.bf[1] + rec * kHeadDim + seg * 16, v);
-        if (WIN && !valid) {   // whatever a masked token holds, nothing of it times weight 0
-#pragma unroll
-            for (int i = 0; i < 16; i++) v[i] = 0.f;
-        }
 #pragma unroll
         for (int gq = 0; gq < GK; gq++) {
             const float p = valid ? exp2f(s_scores[gq * a.chunk + tl] - M[gq]) : 0.f;
@@ -161,7 +170,8 @@ __global__ void __launch_bounds__(128) decode_bf16_kernel(const DecodeArgs a) {
 #pragma unroll 1
         for (int gq = 0; gq < GK; gq++) {
             const size_t row = (size_t)b * a.Hq + hq0 + gq;
-            combine_row(a.partials + row * a.splits_max * kPartialStride, a.S, a.q + row * kHeadDim, a.scale_log2,
+            // 8 splits a batch: 16 would cost the registers of two CTAs an SM
+            combine_row<8>(a.partials + row * a.splits_max * kPartialStride, a.S, a.q + row * kHeadDim, a.scale_log2,
                         nullptr, nullptr, 0, 0, a.out16 ? nullptr : a.out + row * kHeadDim, tid, &s_red[0][0],
                         BlockSync(), TailMask{0, 0}, a.out16 ? a.out16 + row * kHeadDim : nullptr);
         }

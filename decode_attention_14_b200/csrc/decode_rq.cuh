@@ -61,10 +61,14 @@
 // p < sinks: at most two runs of whole 64-token tiles, [0, sinks) and the
 // window's tiles, each dealt over splits of its own, so that a CTA's tokens
 // stay one run.  Tokens of the first window tile before the window are masked
-// (weight zero whatever their records hold).  Their V weights have 28 bits of
+// (weight zero whatever their records hold).  The V weights have 31 bits of
 // fixed point instead of 22: with the high halves then needed for most tokens
-// an 8k b4 call takes 37.1 instead of 35.4 us, and the relative L2 error of the
-// output falls from 2e-4 to 1.5e-6.
+// an 8k b4 call takes 5% longer, and the relative L2 error of the output falls
+// from 2e-4 to 1.5e-6.  The bound is the stream's largest V scale, masked
+// tokens' among them: FP8 scales span 2^-9 .. 448, so 13 bits are left for the
+// visible weights in the worst case (bounding them by the visible tokens'
+// scales, read ahead by the consumers, cost 28% over 64k tokens of 4 query
+// heads a kv head).
 //
 // Thread map (both passes): 4 consumer warps x 16 tokens of each 64-token
 // tile of an item; lane 8s+j takes head_dim segment j (elements 16j..16j+15)
@@ -113,7 +117,7 @@ constexpr int kConsumers = 128;
 constexpr int kThreads = kConsumers + 32;
 constexpr float kRsqrt128 = 0.088388347648318440f;
 constexpr int kWeightTop = 22;                          // V weight bound in [2^21, 2^22) (fixed point)
-constexpr int kWeightTopWin = 28;                       // the windowed call's (sums stay below 2^32: 64 tokens a lane)
+constexpr int kWeightTopWin = 31;                       // the windowed call's (sums of a lane's 64 tokens fit: 2^15 240 64 < 2^31)
 #ifndef RQ_DECODE_PDL
 #define RQ_DECODE_PDL 1
 #endif
@@ -371,7 +375,6 @@ __global__ void __launch_bounds__(kThreads, GK == 1 ? RQ_DECODE_MIN_CTAS : 3) de
     __shared__ int s_abort, s_last;
     __shared__ int s_blk[PG ? kMaxChunk / kTokTile + 1 : 1];   // paged: physical blocks of the chunk
     __shared__ unsigned s_cfmax[NW];
-    __shared__ int s_vmax[WIN ? 1 + NR : 1];   // WIN: largest V scale byte of the visible tokens (anchor, residuals)
     __shared__ float s_q[GK][2][kHeadDim];
     __shared__ __align__(16) uint8_t s_qp[GK][2][3][kHeadDim];   // q byte planes, [plane][segment][word][byte]
     __shared__ int s_qsum[GK][2][8];                             // sum of each segment's fixed-point q
@@ -415,8 +418,6 @@ __global__ void __launch_bounds__(kThreads, GK == 1 ? RQ_DECODE_MIN_CTAS : 3) de
         mbar_init(&bar_cfmax, 31);
         s_abort = 0;
         for (int k = 0; k < NW; k++) s_cfmax[k] = 0;
-        if (WIN)
-            for (int k = 0; k <= NR; k++) s_vmax[k] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
@@ -591,25 +592,6 @@ __global__ void __launch_bounds__(kThreads, GK == 1 ? RQ_DECODE_MIN_CTAS : 3) de
                     atomicMax(&s_cfmax[k], m);
                 }
             }
-            if (WIN) {
-                // the largest V scale among the visible tokens, so that what
-                // masked ones hold does not touch the weights' precision: the
-                // V meta read once here (scales: even bytes, never negative),
-                // which also brings them into L2 for their ring items
-#pragma unroll
-                for (int k = 0; k <= NR; k++) {
-                    const uint8_t *meta = k == 0 ? a.a_meta[1] : a.r_meta[k - 1 < 0 ? 0 : k - 1][1];
-                    uint32_t m = 0;
-#pragma unroll 4
-                    for (int t = lane - 1; t < n; t += 31) {
-                        if (masked(t)) continue;
-                        const uint32_t *p = reinterpret_cast<const uint32_t *>(meta + row_of(t0 + t) * P::MR);
-#pragma unroll
-                        for (int i = 0; i < P::MR / 4; i++) m = __vmaxu2(m, __ldcg(p + i) & 0x00FF00FFu);
-                    }
-                    atomicMax(&s_vmax[k], (int)min(max(m & 0xFFFFu, m >> 16), 0x7Eu));
-                }
-            }
             mbar_arrive(&bar_cfmax);
         }
         return;
@@ -618,11 +600,12 @@ __global__ void __launch_bounds__(kThreads, GK == 1 ? RQ_DECODE_MIN_CTAS : 3) de
     // ------------------------------------------------------------ consumers
     griddep_wait_then_release();
     // upper bounds of this stream's V scales (anchor; the loop's residual)
-    // (WIN: of the split's visible tokens only, found by the producer warp)
-    float vA = WIN ? 0.f : e4m3_to_f32((uint32_t)a.vmax_a[bh]);
+    // (WIN: a NaN scale, byte 0x7F, may belong to a masked token; every other is at most 448)
+    auto bound = [](int byte) { return e4m3_to_f32((uint32_t)(WIN ? min(byte, 0x7E) : byte)); };
+    const float vA = bound(a.vmax_a[bh]);
     float vR[NW];
 #pragma unroll
-    for (int k = 0; k < NW; k++) vR[k] = RESID && !WIN ? e4m3_to_f32((uint32_t)a.vmax_r[k][bh]) : 0.f;
+    for (int k = 0; k < NW; k++) vR[k] = RESID ? bound(a.vmax_r[k][bh]) : 0.f;
     if (a.n_new > 0 && split == 0) {
         // fused append: this unit's new tail rows (K and V, 16-byte vectors);
         // the fence before the arrival count below publishes them to the
@@ -816,11 +799,6 @@ __global__ void __launch_bounds__(kThreads, GK == 1 ? RQ_DECODE_MIN_CTAS : 3) de
     // the records after it on the chain (1 for the last), the anchor's p
     // times the product of all of them; bounds from the coefficients' maxima
     constexpr int top = WIN ? kWeightTopWin : kWeightTop;
-    if (WIN) {
-        vA = e4m3_to_f32((uint32_t)s_vmax[0]);
-#pragma unroll
-        for (int k = 0; k < NR; k++) vR[k] = e4m3_to_f32((uint32_t)s_vmax[k + 1]);
-    }
     float cR[NW];
     float cfprod = 1.f;
 #pragma unroll
