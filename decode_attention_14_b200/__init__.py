@@ -109,6 +109,8 @@ def _load() -> ctypes.CDLL:
     L.rq_cache_export.argtypes = [vp, i32, i32, vp, vp, vp, vp]
     L.rq_decode_attn_window.restype = i32
     L.rq_decode_attn_window.argtypes = [vp, i32, i32, vp, vp, i32, ctypes.c_float, i32, i32, vp]
+    L.rq_prefill_attn_window.restype = i32
+    L.rq_prefill_attn_window.argtypes = [vp, i32, i32, vp, i32, vp, i32, ctypes.c_float, i32, i32, vp]
     i64 = ctypes.c_int64
     L.rq_cache_read.restype = i32
     L.rq_cache_read.argtypes = [vp, i32, i32, i32, i32, i32, vp, vp, i64, i64, i64, vp]
@@ -271,6 +273,12 @@ def rq_decode_attn_window(h, layer: int, loop: int, q, out, out_type: int, softm
                                      softmax_scale, window, sinks, ctypes.c_void_p(_stream(stream)))
 
 
+def rq_prefill_attn_window(h, layer: int, loop: int, q, n_tokens: int, out, out_type: int, softmax_scale: float,
+                           window: int, sinks: int, stream=None) -> int:
+    return lib.rq_prefill_attn_window(h, layer, loop, ctypes.c_void_p(_ptr(q)), n_tokens, ctypes.c_void_p(_ptr(out)),
+                                      out_type, softmax_scale, window, sinks, ctypes.c_void_p(_stream(stream)))
+
+
 def rq_cache_read(h, layer: int, loop: int, t0: int, n_tokens: int, out_type: int, k, v, stride_b: int,
                   stride_t: int, stride_h: int, stream=None) -> int:
     return lib.rq_cache_read(h, layer, loop, t0, n_tokens, out_type, ctypes.c_void_p(_ptr(k)),
@@ -387,7 +395,6 @@ class Cache:
                       scale: float = 0.0, stream=None):
         """rq_decode_attn_window: the last `window` tokens (0: all) and the first `sinks` ones, over either cache
         format; q [batch][num_q_heads][128] bf16 -> `dtype` (float32 unless given, or bfloat16) of the same shape."""
-        import torch
         shape = (self.B, self.Hq, HEAD_DIM)
         _check_dev(q, "bfloat16", shape, "q")
         out = self._window_out(out, dtype, shape, q)
@@ -415,6 +422,19 @@ class Cache:
             out = torch.empty((self.B, n, self.Hq, HEAD_DIM), dtype=torch.float32, device=q.device)
         _check_dev(out, "float32", (self.B, n, self.Hq, HEAD_DIM), "out")
         _ok(rq_prefill_attn(self.h, layer, loop, q, n, out, scale, stream), "rq_prefill_attn")
+        return out
+
+    def prefill_window(self, layer: int, loop: int, q, window: int, sinks: int = 0, out=None, dtype=None,
+                       scale: float = 0.0, stream=None):
+        """rq_prefill_attn_window: the n most recent tokens, each with its last `window` tokens (0: all before it)
+        and the first `sinks` ones; q [batch][n][num_q_heads][128] bf16 -> `dtype` (float32 unless given, or
+        bfloat16) of the same shape."""
+        n = q.shape[1]
+        shape = (self.B, n, self.Hq, HEAD_DIM)
+        _check_dev(q, "bfloat16", shape, "q")
+        out = self._window_out(out, dtype, shape, q)
+        _ok(rq_prefill_attn_window(self.h, layer, loop, q, n, out, _out_type(out.dtype), scale, window, sinks, stream),
+            "rq_prefill_attn_window")
         return out
 
     def append_decode(self, layer: int, loop: int, k, v, q, out=None, scale: float = 0.0, stream=None):

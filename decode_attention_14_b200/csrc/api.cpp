@@ -882,8 +882,53 @@ int rq_decode_attn_window(rq_cache *c, int layer, int loop, const void *q, void 
                          nullptr, 0, nullptr, nullptr, 0, &w);
 }
 
-int rq_prefill_attn(rq_cache *c, int layer, int loop, const void *q, int n, float *out, float scale,
-                    void *stream) {
+}  // extern "C"
+
+namespace {
+
+// Room for `floats` split partials and `units` arrival counters of the
+// multi-token attention, kept by the cache and grown on demand.
+int prefill_workspace(rq_cache *c, size_t floats, size_t units) {
+    if (floats > c->prefill_ws_floats) {
+        if (c->prefill_ws) {
+            if (cudaDeviceSynchronize() != cudaSuccess) return RQ_ERR_CUDA;
+            cudaFree(c->prefill_ws);
+            c->prefill_ws = nullptr;
+            c->prefill_ws_floats = 0;
+        }
+        void *p = nullptr;
+        if (cudaMalloc(&p, floats * sizeof(float)) != cudaSuccess) {
+            cudaGetLastError();
+            return RQ_ERR_NOMEM;
+        }
+        c->prefill_ws = (float *)p;
+        c->prefill_ws_floats = floats;
+    }
+    if (units > c->prefill_cnt_n) {
+        if (c->prefill_cnt) {
+            if (cudaDeviceSynchronize() != cudaSuccess) return RQ_ERR_CUDA;
+            cudaFree(c->prefill_cnt);
+            c->prefill_cnt = nullptr;
+            c->prefill_cnt_n = 0;
+        }
+        void *p = nullptr;
+        if (cudaMalloc(&p, units * sizeof(int)) != cudaSuccess) {
+            cudaGetLastError();
+            return RQ_ERR_NOMEM;
+        }
+        if (cudaMemset(p, 0, units * sizeof(int)) != cudaSuccess) {
+            cudaFree(p);
+            return RQ_ERR_CUDA;
+        }
+        c->prefill_cnt = (int *)p;
+        c->prefill_cnt_n = units;
+    }
+    return RQ_OK;
+}
+
+// win == nullptr: rq_prefill_attn
+int prefill_common(rq_cache *c, int layer, int loop, const void *q, int n, void *out, float scale, void *stream,
+                   const WindowSpec *win) {
     if (!c || !q || !out || n <= 0) return RQ_ERR_INVALID;
     if (!on_cache_device(c)) return RQ_ERR_INVALID;
     const Layout &L = c->lay;
@@ -919,7 +964,7 @@ int rq_prefill_attn(rq_cache *c, int layer, int loop, const void *q, int n, floa
     for (int b = 0; b < cfg.batch; b++)
         if (a.seqT.v[b] + a.n_tail < n) return RQ_ERR_STATE;
     a.q = (const uint16_t *)q;
-    a.out = out;
+    a.out = (float *)out;
     a.B = cfg.batch;
     a.H = cfg.num_kv_heads;
     a.Hq = cfg.num_q_heads;
@@ -932,51 +977,42 @@ int rq_prefill_attn(rq_cache *c, int layer, int loop, const void *q, int n, floa
     a.rotate = cfg.rotate;
     std::memcpy(a.sigma, &c->sigma[(size_t)layer * 4], sizeof(a.sigma));
     if (n > 65535) return RQ_ERR_UNSUPPORTED;   // grid limit
-    prefill_plan(&a, T, cfg.anchor_bits, cfg.resid_bits, c->sms);
+    if (win) {
+        a.window = win->window;
+        a.sinks = win->sinks;
+        if (win->out_type == RQ_OUT_BF16) {
+            a.out16 = (uint16_t *)out;
+            a.out = nullptr;
+        }
+        prefill_window_plan(&a, c->sms);
+    } else {
+        prefill_plan(&a, T, cfg.anchor_bits, cfg.resid_bits, c->sms);
+    }
     if ((long)a.B * a.nqb > 65535) return RQ_ERR_UNSUPPORTED;
-    const size_t need = (size_t)a.B * n * a.Hq * std::max(a.S, 1) * kPartialStride;
-    if (need > c->prefill_ws_floats) {
-        if (c->prefill_ws) {
-            if (cudaDeviceSynchronize() != cudaSuccess) return RQ_ERR_CUDA;
-            cudaFree(c->prefill_ws);
-            c->prefill_ws = nullptr;
-            c->prefill_ws_floats = 0;
-        }
-        void *p = nullptr;
-        if (cudaMalloc(&p, need * sizeof(float)) != cudaSuccess) {
-            cudaGetLastError();
-            return RQ_ERR_NOMEM;
-        }
-        c->prefill_ws = (float *)p;
-        c->prefill_ws_floats = need;
-    }
+    // a windowed call of one split writes its rows directly
+    const bool direct = win && a.S == 1;
+    const int s = prefill_workspace(c, direct ? 0 : (size_t)a.B * n * a.Hq * std::max(a.S, 1) * kPartialStride,
+                                    direct || a.S == 0 ? 0 : (size_t)a.B * a.H * a.nqb);
+    if (s != RQ_OK) return s;
     a.partials = c->prefill_ws;
-    a.counters = nullptr;
-    if (a.S > 0) {
-        const size_t units = (size_t)a.B * a.H * a.nqb;
-        if (units > c->prefill_cnt_n) {
-            if (c->prefill_cnt) {
-                if (cudaDeviceSynchronize() != cudaSuccess) return RQ_ERR_CUDA;
-                cudaFree(c->prefill_cnt);
-                c->prefill_cnt = nullptr;
-                c->prefill_cnt_n = 0;
-            }
-            void *p = nullptr;
-            if (cudaMalloc(&p, units * sizeof(int)) != cudaSuccess) {
-                cudaGetLastError();
-                return RQ_ERR_NOMEM;
-            }
-            if (cudaMemset(p, 0, units * sizeof(int)) != cudaSuccess) {
-                cudaFree(p);
-                return RQ_ERR_CUDA;
-            }
-            c->prefill_cnt = (int *)p;
-            c->prefill_cnt_n = units;
-        }
-        a.counters = c->prefill_cnt;
-    }
+    a.counters = a.S > 0 ? c->prefill_cnt : nullptr;
     a.err = (int *)(c->base + L.off_err);
     return cuda_status(launch_prefill(a, cfg.anchor_bits, cfg.resid_bits, (cudaStream_t)stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+int rq_prefill_attn(rq_cache *c, int layer, int loop, const void *q, int n, float *out, float scale, void *stream) {
+    return prefill_common(c, layer, loop, q, n, out, scale, stream, nullptr);
+}
+
+int rq_prefill_attn_window(rq_cache *c, int layer, int loop, const void *q, int n, void *out, int out_type, float scale,
+                           int window, int sinks, void *stream) {
+    WindowSpec w;
+    if (!c || !window_spec(window, sinks, out_type, &w)) return RQ_ERR_INVALID;
+    return prefill_common(c, layer, loop, q, n, out, scale, stream, &w);
 }
 
 int rq_cache_length(const rq_cache *c, int layer, int group, int *len) {

@@ -33,11 +33,42 @@ struct PrefillArgs {
                                        // split of a row block merges the partials; null: the
                                        // combine kernel merges them
     int tail_in_kernel;                // the attention kernel (last split) takes the tail tokens
+    int window, sinks;                 // windowed calls: the query at position p sees (p - window, p] and [0, sinks)
+    uint16_t *out16;                   // the output in BF16 instead of `out`, or null
 };
+
+// What the rows of query tokens [i0, i1] of a windowed call see of a sequence
+// of T committed and n_tail tail tokens, as runs that whole 64-token tiles of
+// are read: committed [0, sink_end) and [w_tile, lim) (the first row's window
+// begins at w0), tail tokens [tail0, tail1).  The runs are dealt over the
+// splits as one, the sinks' padded to a tile.
+struct BlockRuns {
+    int sink_end, w_tile, w0, lim, tail0, tail1;
+    __host__ __device__ int sink_pad() const { return (sink_end + kTokTile - 1) / kTokTile * kTokTile; }
+    __host__ __device__ int committed() const { return sink_pad() + (lim - w_tile + kTokTile - 1) / kTokTile * kTokTile; }
+    __host__ __device__ int total() const { return committed() + tail1 - tail0; }
+};
+__host__ __device__ inline BlockRuns block_runs(int T, int n_tail, int n, int i0, int i1, int window, int sinks) {
+    BlockRuns r;
+    const long long p0 = (long long)T + n_tail - n + i0, p1 = (long long)T + n_tail - n + i1;   // positions
+    const long long first = p0 + 1 - window;                                                    // of row i0's window
+    r.lim = (int)(p1 + 1 < T ? p1 + 1 : T);
+    r.w0 = (int)(first < 0 ? 0 : first > r.lim ? r.lim : first);
+    r.w_tile = r.w0 == r.lim ? r.lim : r.w0 / kTokTile * kTokTile;
+    r.sink_end = sinks < r.w_tile ? sinks : r.w_tile;
+    r.tail1 = p1 + 1 > T ? (int)(p1 + 1 - T) : 0;
+    r.tail0 = first > T && sinks <= T ? (int)(first - T) / kPrefillTile * kPrefillTile : 0;
+    if (r.tail0 > r.tail1) r.tail0 = r.tail1;
+    return r;
+}
 
 // Sets a->nqb and the split count a->S over the committed tokens (T
 // = the longest sequence); a->B, H, G and n must be set.
 void prefill_plan(PrefillArgs *a, int T, int ba, int br, int sms);
+// The same for a windowed call (a->window, a->sinks, a->n_tail and a->seqT set).
+void prefill_window_plan(PrefillArgs *a, int sms);
+cudaError_t launch_prefill_window(const PrefillArgs &a, int ba, int br, cudaStream_t st);
+// a.window > 0: windowed
 cudaError_t launch_prefill(const PrefillArgs &a, int ba, int br, cudaStream_t st);
 
 }  // namespace rq

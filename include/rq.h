@@ -295,6 +295,28 @@ int rq_decode_attn_window(rq_cache *cache, int layer, int loop, const void *q_bf
                           float softmax_scale, int window, int sinks, void *stream);
 
 /*
+ * Attention of several new tokens with a sliding window and sinks, over either
+ * cache format: the n most recent tokens of every sequence, each attending --
+ * from its own position p of the sequence [committed tokens, tail tokens] --
+ * to positions (p - window, p] and to the first `sinks` positions.  For
+ * RQ_FMT_BF16 caches (whose appends commit at once: the n new tokens are the
+ * last committed ones) it is also, with window 0, the plain causal attention
+ * of a prefill chunk.
+ *   q_bf16: device, [batch][n_tokens][num_q_heads][head_dim] BF16, oldest first.
+ *   out:    device, the same shape, of out_type (rq_out_type).
+ *   window, sinks, softmax_scale: as for rq_decode_attn_window.
+ * A masked token does not enter a row, whatever it holds.
+ * The split partials and arrival counters are rq_prefill_attn's buffers, under
+ * the same rules (make the first call of a size before any stream capture);
+ * a call whose row blocks fill the device by themselves needs neither.
+ * Errors: INVALID (null pointer, n_tokens < 1, index, window < 0, sinks < 0,
+ * out_type), STATE (a sequence holds fewer than n_tokens tokens), UNSUPPORTED
+ * (as rq_prefill_attn), NOMEM, CUDA.
+ */
+int rq_prefill_attn_window(rq_cache *cache, int layer, int loop, const void *q_bf16, int n_tokens, void *out,
+                           int out_type, float softmax_scale, int window, int sinks, void *stream);
+
+/*
  * rq_decode_attn without any allocation: identical arguments, results and
  * errors, except that the split-combine partials go to a fixed array the
  * library holds in device memory (8 MiB per GPU that loads the library, kept

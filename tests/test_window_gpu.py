@@ -281,3 +281,173 @@ def test_window_refusals():
     with pytest.raises(rq.RQError):
         bt.cache.decode_window(0, 0, q, -4)
     bt.cache.close()
+
+
+# ------------------------------------------------------------------ several tokens
+def chunk_check(bt, loop, lens, n, window, sinks, dtype=torch.float32, seed=11, rel=1e-3, mx=2e-3):
+    q = queries(seed, bt.cfg.batch, n, bt.cfg.num_q_heads, 128)
+    ref = reference(keys_values(bt, 0, loop, lens), q, window, sinks)
+    check(bt.cache.prefill_window(0, loop, q, window, sinks, dtype=dtype), ref, rel, mx)
+
+
+@pytest.mark.parametrize("T,n", [(1, 1), (40, 7), (64, 64), (65, 33), (200, 130), (700, 1), (700, 65), (1000, 300)])
+@pytest.mark.parametrize("Hq", [2, 8])
+def test_prefill_windows(T, n, Hq):
+    """A committed chunk (the anchor loop) and one in the tail (a residual loop), T - n tokens before it."""
+    bt = H.build(T=T, H=2, Hq=Hq, seed=0x5EEDCC01, n_tail=n, max_tokens=T + 1)
+    for window, sinks in ((1, 0), (5, 2), (32, 0), (64, 4), (100, 70), (257, 3), (0, 0), (BIG, 0), (640, 700)):
+        chunk_check(bt, 3, [T], n, window, sinks)
+        chunk_check(bt, 1, [T], n, window, sinks, torch.bfloat16)
+    bt.cache.check()
+    bt.cache.close()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(g=32), dict(ba=2), dict(br=4, g=32), dict(rotate=False), dict(Hq=16), dict(loops=2, Lg=1),
+    dict(B=3, block_tokens=128, num_blocks=24, prepare=lambda c: c.shuffle_free_blocks(5)),
+    dict(B=2, block_tokens=256, num_blocks=8, prepare=lambda c: c.shuffle_free_blocks(6), Hq=8),
+], ids=lambda kw: "-".join(f"{k}{v}" for k, v in kw.items() if k != "prepare"))
+def test_prefill_window_variants(kw):
+    bt = H.build(**{"T": 700, "n_tail": 70, "H": 2, "Hq": 4, "seed": 0x5EEDCC02, **kw})
+    for loop in range(bt.cfg.num_loops):
+        for window, sinks in ((300, 4), (64, 130), (33, 0)):
+            n = 150 if loop % bt.cfg.loops_per_group == bt.cfg.loops_per_group - 1 else 70
+            chunk_check(bt, loop, [700] * bt.cfg.batch, n, window, sinks)
+    bt.cache.check()
+    bt.cache.close()
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_prefill_windows_of_ragged_sequences(paged):
+    kw = dict(block_tokens=128, num_blocks=48, prepare=lambda c: c.shuffle_free_blocks(3)) if paged else {}
+    bt = H.build(B=5, T=1100, H=2, Hq=4, seed=0x5EEDCC03, **kw)
+    lens = [1100, 64, 40, 130, 129]
+    for b in range(5):
+        bt.cache.truncate_seq(0, 0, b, lens[b])
+    for window, sinks in ((1, 0), (3, 1), (64, 4), (66, 200), (500, 64), (0, 0)):
+        chunk_check(bt, 3, lens, 40, window, sinks)
+    bt.cache.truncate_seq(0, 0, 2, 0)
+    lens[2] = 0
+    K, V = bt.inputs[(0, 0)]
+    tail = torch.randn((2, 5, 90, 2, 128), device="cuda", generator=torch.Generator("cuda").manual_seed(1)).bfloat16()
+    bt.cache.append(0, 1, tail[0].contiguous(), tail[1].contiguous())
+    bt.inputs[(0, 0)] = tuple([torch.cat((X[j], tail[i]), 1) for j in range(4)] for i, X in ((0, K), (1, V)))
+    bt.n_tail = 90
+    for n in (1, 33, 90):                    # all of the tail, and its last part
+        for window, sinks in ((1, 0), (3, 1), (64, 4), (66, 200), (500, 64), (30, 1200), (0, 0)):
+            chunk_check(bt, 1, lens, n, window, sinks)
+    bt.cache.check()
+    bt.cache.close()
+
+
+def test_prefill_window_of_a_cache_without_committed_tokens():
+    """The first chunk of a prompt at a residual loop: everything is in the tail."""
+    bt = H.build(T=0, n_tail=500, B=2, H=2, Hq=4, max_tokens=64, seed=0x5EEDCC04)
+    for n in (1, 200, 500):
+        for window, sinks in ((1, 0), (64, 4), (100, 450), (0, 0)):
+            q = queries(12, 2, n, 4, 128)
+            kv = [np.stack([orc.bf16_bits_to_f64(synth.bf16_to_u16(bt.inputs[(0, 0)][i][0][b:b + 1]))[0].transpose(1, 0, 2)
+                            for i in range(2)]) for b in range(2)]
+            check(bt.cache.prefill_window(0, 0, q, window, sinks), reference(kv, q, window, sinks), 1e-3, 2e-3)
+    bt.cache.check()
+    bt.cache.close()
+
+
+def test_a_chunk_longer_than_its_window():
+    """Row blocks that see neither the chunk's beginning nor its end, one split each; window and sinks apart."""
+    bt = H.build(T=600, n_tail=1500, H=16, Hq=16, seed=0x5EEDCC05, chunk=300, max_tokens=2200)
+    chunk_check(bt, 0, [600], 1500, 200, 10)
+    chunk_check(bt, 0, [600], 1500, 700, 0, torch.bfloat16)
+    bt.cache.check()
+    bt.cache.close()
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf"), 3e38])
+@pytest.mark.parametrize("where", ["committed", "tail"])
+def test_prefill_does_not_see_what_masked_tokens_hold(where, value):
+    """One poisoned token, in K and V: rows that do not see it are as if it held zeros; rows that do may be anything."""
+    T, n = 300, 80
+    bt = H.build(T=T, H=2, Hq=4, seed=0x5EEDCC06, n_tail=n, max_tokens=512)
+    K, V = ([x.clone() for x in X] for X in bt.inputs[(0, 0)])
+    at = 250 if where == "committed" else T + 30
+    for X in (K, V):
+        for x in X:
+            x[:, at] = value
+    ref_in = tuple([x.clone() for x in X] for X in bt.inputs[(0, 0)])
+    kv0 = {loop: keys_values(bt, 0, loop, [T]) for loop in (0, 3)}
+    bt.cache.append(0, 3, *[x[3][:, T:].contiguous() for x in ref_in])     # commits the tails, so that it can be emptied
+    bt.cache.truncate(0, 0, 0)
+    bt.recon.clear()
+    H.fill_group(bt, 0, 0, K, V, 64)
+    bt.inputs[(0, 0)] = ref_in
+    window, sinks = 40, 5
+    for loop in (0, 3):
+        P = T + (n if loop == 0 else 0)
+        m = n if loop == 0 else 120
+        q = queries(13, 1, m, 4, 128)
+        ref = reference(kv0[loop], q, window, sinks)
+        got = bt.cache.prefill_window(0, loop, q, window, sinks).double().cpu().numpy()
+        pos = np.arange(P - m, P)
+        blind = (at > pos) | ((at <= pos - window) & (at >= sinks))
+        assert blind.any()
+        assert np.isfinite(got[:, blind]).all()
+        far = np.abs(got[:, blind] - ref[:, blind])
+        assert far.max() <= 2e-3 and np.linalg.norm(far) <= 1e-3 * np.linalg.norm(ref[:, blind])
+        if np.isnan(value) and (~blind).any():
+            assert np.isnan(got[:, ~blind]).all()      # where it is seen, it shows
+    bt.cache.close()
+
+
+def test_prefill_window_equals_itself_in_any_order_of_calls():
+    bt = H.build(B=2, T=900, H=2, Hq=4, n_tail=40, seed=0x5EEDCC07)
+    q = queries(14, 2, 40, 4, 128)
+    first = bt.cache.prefill_window(0, 1, q, 333, 4)
+    # window 0 is rq_prefill_attn; one token is the single-token call
+    check(bt.cache.prefill_window(0, 1, q, 0), bt.cache.prefill(0, 1, q).double().cpu().numpy(), 1e-4, 1e-3)
+    one = bt.cache.prefill_window(0, 1, q[:, -1:].contiguous(), 333, 4)
+    check(one, bt.cache.decode_window(0, 1, q[:, -1].contiguous(), 333, 4)[:, None].double().cpu().numpy(), 1e-4, 1e-3)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out = torch.zeros_like(first)
+    bt.cache.prefill_window(0, 1, q, 333, 4, out=out, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(out, first)
+    g = torch.cuda.CUDAGraph()
+    out2 = torch.zeros_like(first)
+    with torch.cuda.graph(g):
+        bt.cache.prefill_window(0, 2, q, 50, 0)
+        bt.cache.prefill_window(0, 1, q, 333, 4, out=out2)
+    for _ in range(3):
+        out2.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out2, first)
+        bt.cache.prefill(0, 1, q)
+        assert torch.equal(bt.cache.prefill_window(0, 1, q, 333, 4), first)
+    bt.cache.check()
+    bt.cache.close()
+
+
+def test_prefill_window_refusals():
+    bt = H.build(T=20, n_tail=4, H=2, Hq=2, seed=0x5EEDCC09)
+    q, out = queries(8, 1, 4, 2, 128), torch.zeros((1, 4, 2, 128), device="cuda")
+
+    def call(layer=0, loop=0, qq=q, n=4, oo=out, kind=rq.RQ_OUT_FP32, window=4, sinks=1):
+        return rq.rq_prefill_attn_window(bt.cache.h, layer, loop, qq, n, oo, kind, 0.0, window, sinks)
+
+    assert call() == rq.RQ_OK
+    for kw in (dict(layer=1), dict(layer=-1), dict(loop=4), dict(loop=-1), dict(qq=None), dict(oo=None), dict(kind=2),
+               dict(n=0), dict(n=-1), dict(window=-1), dict(sinks=-1)):
+        assert call(**kw) == rq.RQ_ERR_INVALID, kw
+    assert call(n=25) == rq.RQ_ERR_STATE and call(loop=3, n=21) == rq.RQ_ERR_STATE
+    with pytest.raises(ValueError):
+        bt.cache.prefill_window(0, 0, q[:, :, :1], 4)
+    with pytest.raises(ValueError):
+        bt.cache.prefill_window(0, 0, q, 4, out=out, dtype=torch.bfloat16)
+    for kw in (dict(ba=2, br=4), dict(anchor_mode=rq.ANCHOR_CHAINED)):
+        other = H.build(T=20, H=2, Hq=2, seed=0x5EEDCC0A, **kw)
+        with pytest.raises(rq.RQError) as e:
+            other.cache.prefill_window(0, 3, q, 4)
+        assert e.value.status == rq.RQ_ERR_UNSUPPORTED
+        other.cache.close()
+    bt.cache.close()
