@@ -116,6 +116,9 @@ int *vmax_ptr(const rq_cache *c, int layer, int group, int r) {
     return (int *)(c->base + L.off_vmax) + (((size_t)layer * L.groups + group) * L.Lg + r) * bh;
 }
 
+// whether a V value that is not finite was ever stored (BF16 format)
+int *nonfinite_ptr(const rq_cache *c) { return (int *)(c->base + c->lay.off_err) + 1; }
+
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? RQ_OK : RQ_ERR_CUDA; }
 
 // Token -> record row mapping of the compressed format.
@@ -604,6 +607,7 @@ int rq_append(rq_cache *c, int layer, int loop, const void *k, const void *v, in
         a.n = n;
         fill_lens(seq_lens(c, slot), cfg.batch, &a.pos0);
         a.Tp = L.Tp;
+        a.nonfinite = nonfinite_ptr(c);
         int s = cuda_status(launch_bf16_store(a, st));
         if (s == RQ_OK) grow(c, slot, n);
         return s;
@@ -888,7 +892,14 @@ namespace {
 
 // Room for `floats` split partials and `units` arrival counters of the
 // multi-token attention, kept by the cache and grown on demand.
-int prefill_workspace(rq_cache *c, size_t floats, size_t units) {
+// While `st` is being captured nothing can be allocated: NOMEM, the capture
+// left valid.
+int prefill_workspace(rq_cache *c, size_t floats, size_t units, cudaStream_t st) {
+    if (st && (floats > c->prefill_ws_floats || units > c->prefill_cnt_n)) {
+        cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+        if (cudaStreamIsCapturing(st, &cap) != cudaSuccess) return RQ_ERR_CUDA;
+        if (cap != cudaStreamCaptureStatusNone) return RQ_ERR_NOMEM;
+    }
     if (floats > c->prefill_ws_floats) {
         if (c->prefill_ws) {
             if (cudaDeviceSynchronize() != cudaSuccess) return RQ_ERR_CUDA;
@@ -934,23 +945,24 @@ int prefill_common(rq_cache *c, int layer, int loop, const void *q, int n, void 
     const Layout &L = c->lay;
     const rq_config &cfg = L.cfg;
     if (layer < 0 || layer >= cfg.num_layers || loop < 0 || loop >= cfg.num_loops) return RQ_ERR_INVALID;
-    if (cfg.format != RQ_FMT_RESIDUAL) return RQ_ERR_STATE;
+    const bool bf16 = cfg.format == RQ_FMT_BF16;
+    if (bf16 && !win) return RQ_ERR_STATE;
     // the multi-token kernel is built for INT4/INT2, INT2/INT2 and INT4/INT4,
     // the last-loop reference (contiguous or paged records)
-    if (cfg.anchor_bits == 2 && cfg.resid_bits == 4) return RQ_ERR_UNSUPPORTED;
+    if (!bf16 && cfg.anchor_bits == 2 && cfg.resid_bits == 4) return RQ_ERR_UNSUPPORTED;
     if (cfg.anchor_mode != 0) return RQ_ERR_UNSUPPORTED;
     PrefillArgs a;
     std::memset(&a, 0, sizeof(a));
     const int group = loop / L.Lg, j = loop % L.Lg;
-    const size_t slot = (size_t)layer * L.groups + group;
+    const size_t slot = bf16 ? (size_t)layer * cfg.num_loops + loop : (size_t)layer * L.groups + group;
     const int T = c->len[slot];
     fill_lens(seq_lens(c, slot), cfg.batch, &a.seqT);
     a.pg = pages_of(c);
-    for (int kv = 0; kv < 2; kv++) {
+    for (int kv = 0; kv < 2 && !bf16; kv++) {
         a.a_codes[kv] = anchor_codes(c, layer, group, kv);
         a.a_meta[kv] = anchor_meta(c, layer, group, kv);
     }
-    if (!is_commit_loop(L, loop)) {
+    if (!bf16 && !is_commit_loop(L, loop)) {
         for (int kv = 0; kv < 2; kv++) {
             a.r_codes[kv] = resid_codes(c, layer, group, j, kv);
             a.r_meta[kv] = resid_meta(c, layer, group, j, kv);
@@ -984,7 +996,8 @@ int prefill_common(rq_cache *c, int layer, int loop, const void *q, int n, void 
             a.out16 = (uint16_t *)out;
             a.out = nullptr;
         }
-        prefill_window_plan(&a, c->sms);
+        if (bf16) prefill_bf16_plan(&a, c->sms);
+        else prefill_window_plan(&a, c->sms);
     } else {
         prefill_plan(&a, T, cfg.anchor_bits, cfg.resid_bits, c->sms);
     }
@@ -992,11 +1005,14 @@ int prefill_common(rq_cache *c, int layer, int loop, const void *q, int n, void 
     // a windowed call of one split writes its rows directly
     const bool direct = win && a.S == 1;
     const int s = prefill_workspace(c, direct ? 0 : (size_t)a.B * n * a.Hq * std::max(a.S, 1) * kPartialStride,
-                                    direct || a.S == 0 ? 0 : (size_t)a.B * a.H * a.nqb);
+                                    direct || a.S == 0 ? 0 : (size_t)a.B * a.H * a.nqb, (cudaStream_t)stream);
     if (s != RQ_OK) return s;
     a.partials = c->prefill_ws;
     a.counters = a.S > 0 ? c->prefill_cnt : nullptr;
     a.err = (int *)(c->base + L.off_err);
+    if (bf16)
+        return cuda_status(launch_prefill_bf16(a, bf16_ptr(c, layer, loop, 0), bf16_ptr(c, layer, loop, 1),
+                                               nonfinite_ptr(c), c->sms, (cudaStream_t)stream));
     return cuda_status(launch_prefill(a, cfg.anchor_bits, cfg.resid_bits, (cudaStream_t)stream));
 }
 

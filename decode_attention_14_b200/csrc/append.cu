@@ -275,7 +275,15 @@ __global__ void bf16_store_kernel(const Bf16StoreArgs a) {
     const int b = (int)(r / a.n);
     const uint4 *src = reinterpret_cast<const uint4 *>(a.src[kv] + (((size_t)b * a.n + t) * a.H + h) * kHeadDim);
     uint4 *dst = reinterpret_cast<uint4 *>(a.dst[kv] + (((size_t)b * a.H + h) * a.Tp + a.pos0.v[b] + t) * kHeadDim);
-    dst[vec] = src[vec];
+    const uint4 v = src[vec];
+    dst[vec] = v;
+    // a V that is not finite (exponent all ones) is noted: the tensor-core
+    // attention then keeps it from rows that do not see it
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t bad = 0;
+#pragma unroll
+    for (int k = 0; k < 4; k++) bad |= ((w[k] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+    if (kv == 1 && bad) *a.nonfinite = 1;
 }
 
 // Paged caches: block-table writes (CTA (0, 0)) and block copies (CTA

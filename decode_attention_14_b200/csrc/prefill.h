@@ -71,4 +71,10 @@ cudaError_t launch_prefill_window(const PrefillArgs &a, int ba, int br, cudaStre
 // a.window > 0: windowed
 cudaError_t launch_prefill(const PrefillArgs &a, int ba, int br, cudaStream_t st);
 
+// Attention of several new tokens over a BF16 cache (prefill_bf16.cu): k, v
+// [B * H][Tp][d]; a->nqb and a->S are the plan's; tail and record fields unused.
+void prefill_bf16_plan(PrefillArgs *a, int sms);
+cudaError_t launch_prefill_bf16(const PrefillArgs &a, const uint16_t *k, const uint16_t *v, const int *nonfinite, int sms,
+                                cudaStream_t st);
+
 }  // namespace rq

@@ -1,0 +1,620 @@
+// prefill_bf16.cu -- attention of several new tokens over the uncompressed cache
+// (rq_prefill_attn_window on RQ_FMT_BF16): causal, with an optional sliding
+// window and sinks.  The query at position p sees (p - window, p] and
+// [0, sinks).
+//
+//   z = q K^T scale,  out = sum_t 2^(z_t - m) v_t / sum_t 2^(z_t - m)
+// in one pass over the keys, with a running maximum m that is raised only when
+// a row's maximum grows by more than 2^8 (then the row's accumulated output is
+// rescaled), as in prefill.cuh.
+//
+// CTA = (split of the tokens, kv head, sequence x block of QT * 128 query rows,
+// row = query token x head of the group).  Per 128-token tile and 128 rows, on
+// the tcgen05 tensor cores:
+//   S = Q K^T   8 MMAs of 128x128x16, both operands from shared memory
+//   O += P V    8 MMAs of 128x128x16 with P from tensor memory (16 with SPLIT:
+//               P as a BF16 high and low part, relative 2^-17, for fp32 output;
+//               for BF16 output P is rounded to BF16, half a step of which,
+//               2^-9 of each weight, is as small as the output's own rounding)
+// P overwrites S in tensor memory: S (128 columns) and O (128) per row tile.
+// With QT = 2 one row tile's MMAs run while the other's softmax does, and both
+// share every K and V tile, which halves the L2 traffic (a 128 x 128 tile pair
+// is 64 KB for 2 x 1024 tensor cycles); with QT = 1 two CTAs share an SM.
+//
+// Warps: 4 QT softmax warps (a thread per row: tensor-memory lane = row), then
+// one that issues the TMA loads (K and V tiles alternate in a ring of
+// 128-byte-swizzled 32 KB stages) and one that issues the MMAs.
+// Hand-offs, all bounded waits (error word, abort flag):
+//   full[s]   TMA -> MMA          stage s loaded
+//   empty[s]  MMA commit -> TMA   stage s read
+//   sfull[q]  MMA commit -> softmax   S of row tile q complete, and with it all
+//             MMAs issued before, the values of the tile before among them
+//   pfull[q]  softmax -> MMA      P of row tile q written
+//   ofull[q]  MMA commit -> softmax   the last values complete
+//
+// A V row that only some rows see may hold NaN or infinities, which 0 * NaN
+// would carry into the other rows.  The store kernel notes in the arena when it
+// was ever given such a V (a.nonfinite); only then, the first softmax warps look
+// every V tile over before its values are formed, zero such rows and flag them,
+// and rows that do see one get a NaN weight.  (A NaN in K stays in the token's
+// own logits, which the rows that do not see it replace.)
+#include <cuda.h>
+#include <math_constants.h>
+
+#include <algorithm>
+
+#include "combine.cuh"
+#include "common.cuh"
+#include "prefill.h"
+#include "sync.cuh"
+#include "tc.cuh"
+
+namespace rq {
+namespace {
+
+constexpr int kTileT = 128;                          // tokens per tile
+constexpr int kTileR = 128;                          // rows per row tile
+constexpr int kBlkBytes = 128 * 128;                 // 128 rows of 64 BF16 columns
+constexpr int kStageBytes = 2 * kBlkBytes;           // a K or V tile, or a Q row tile
+constexpr float kRaiseLog2 = 8.f;
+
+template <int QT>
+struct Cfg {
+    static constexpr int STAGES = QT == 2 ? 5 : 2;
+    static constexpr int THREADS = 32 * (4 * QT + 2);
+    static constexpr int CTAS = QT == 2 ? 1 : 2;
+    static constexpr int SMEM = (QT + STAGES) * kStageBytes + 1024;   // + alignment of the base
+    static constexpr uint32_t COLS = 256 * QT;       // S and O of each row tile
+};
+
+// ---------------------------------------------------------------- PTX helpers
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void expect_tx(uint64_t *bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+// D[tmem] (+)= A[tmem] B[smem]: A is M lanes x K / 2 columns of BF16 pairs.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+#define RQ_R32(v) \
+    "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), \
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), \
+        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), \
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+#define RQ_W32(c, v) \
+    c(v[0]), c(v[1]), c(v[2]), c(v[3]), c(v[4]), c(v[5]), c(v[6]), c(v[7]), c(v[8]), c(v[9]), c(v[10]), c(v[11]), \
+        c(v[12]), c(v[13]), c(v[14]), c(v[15]), c(v[16]), c(v[17]), c(v[18]), c(v[19]), c(v[20]), c(v[21]), c(v[22]), \
+        c(v[23]), c(v[24]), c(v[25]), c(v[26]), c(v[27]), c(v[28]), c(v[29]), c(v[30]), c(v[31])
+#define RQ_OUT_REG(x) "=r"(x)
+#define RQ_INOUT_REG(x) "+r"(x)
+// 32 consecutive columns of the warp's 32 lanes (usable after wait_ld / settle)
+__device__ __forceinline__ void ld32(uint32_t taddr, uint32_t *v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : RQ_W32(RQ_OUT_REG, v)
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void st32(uint32_t taddr, const uint32_t *v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        RQ_R32(v)
+        : "memory");
+}
+__device__ __forceinline__ void wait_ld32(uint32_t *v) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : RQ_W32(RQ_INOUT_REG, v)::"memory");
+}
+// no use of v is scheduled before this point (and so not before a wait above it)
+__device__ __forceinline__ void settle32(uint32_t *v) { asm volatile("" : RQ_W32(RQ_INOUT_REG, v)::"memory"); }
+
+__device__ __forceinline__ float ex2f(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float x0, float x1) {   // x0 in the low half
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(x1), "f"(x0));
+    return d;
+}
+// bits [lo, hi) of a 32-bit word (clamped)
+__device__ __forceinline__ uint32_t range_bits(int lo, int hi) {
+    lo = max(lo, 0);
+    hi = min(hi, 32);
+    return hi <= lo ? 0u : (0xFFFFFFFFu >> (32 - (hi - lo))) << lo;
+}
+
+struct Bf16Args {
+    const uint16_t *q;      // [B][n][Hq][d]
+    float *partials;        // [B][n][Hq][S][kPartialStride]
+    float *out;             // [B][n][Hq][d] fp32, or
+    uint16_t *out16;        // BF16
+    int *counters;          // [B][H][nqb] split arrivals
+    int *err;
+    const int *nonfinite;   // a V that is not finite was ever stored
+    SeqLens seqT;
+    int B, H, Hq, G, n, S, nqb;
+    int window, sinks;
+    float scale_log2;
+};
+
+// The token runs that rows of query tokens [i0, i1] read, in tiles of 128.
+struct Runs {
+    int sink_tiles, w_tile, tiles;
+    __host__ __device__ Runs(int T, int n, int i0, int i1, int window, int sinks) {
+        const BlockRuns r = block_runs(T, 0, n, i0, i1, window, sinks);
+        w_tile = r.w_tile;
+        sink_tiles = (r.sink_end + kTileT - 1) / kTileT;
+        tiles = sink_tiles + (r.lim - r.w_tile + kTileT - 1) / kTileT;
+    }
+    __host__ __device__ int token(int tile) const {
+        return tile < sink_tiles ? tile * kTileT : w_tile + (tile - sink_tiles) * kTileT;
+    }
+};
+
+template <int QT, bool SPLIT>
+__global__ void __launch_bounds__(Cfg<QT>::THREADS, Cfg<QT>::CTAS)
+    prefill_bf16_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                        const Bf16Args a) {
+    using C = Cfg<QT>;
+    constexpr int NS = C::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t bar_full[NS], bar_empty[NS], bar_sfull[QT], bar_pfull[QT], bar_ofull[QT];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort, s_last;
+    __shared__ uint8_t s_bad[kTileT];
+
+    const uint32_t raw_base = smem_u32(smem_raw);
+    uint8_t *sm = smem_raw + (((raw_base + 1023u) & ~1023u) - raw_base);   // Q row tiles, then the stages
+    const uint32_t sbase = smem_u32(sm);
+    uint8_t *stages = sm + QT * kStageBytes;
+    const uint32_t sstage = sbase + QT * kStageBytes;
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int split = blockIdx.x, h = blockIdx.y;
+    const int b = blockIdx.z / a.nqb, qb = a.nqb - 1 - blockIdx.z % a.nqb;   // the longest row blocks first
+    const int r0 = qb * QT * kTileR;
+    const int nr = min(QT * kTileR, a.n * a.G - r0);
+    const int Tb = a.seqT.v[b];
+    const Runs runs(Tb, a.n, r0 / a.G, (r0 + nr - 1) / a.G, a.window, a.sinks);
+    // this split's tiles
+    const int j0 = (int)((long long)split * runs.tiles / a.S), j1 = (int)((long long)(split + 1) * runs.tiles / a.S);
+    const int nt = j1 - j0;
+
+    if (tid == 0) {
+        for (int i = 0; i < NS; i++) {
+            mbar_init(&bar_full[i], 1);
+            mbar_init(&bar_empty[i], 1);
+        }
+        for (int i = 0; i < QT; i++) {
+            mbar_init(&bar_sfull[i], 1);
+            mbar_init(&bar_pfull[i], 4);   // a lane of each of its softmax warps
+            mbar_init(&bar_ofull[i], 1);
+        }
+        s_abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 4 * QT + 1) {
+        tc::alloc(&s_tmem, C::COLS);
+        tc::relinquish();
+    }
+    // Q rows, 16-byte chunks swizzled as TMA does; rows past nr are zero
+    for (int i = tid; i < QT * kTileR * 16; i += C::THREADS) {
+        const int row = i >> 4, c = i & 15;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (row < nr) {
+            const int rg = r0 + row, t = rg / a.G, gq = rg % a.G;
+            v = __ldg(reinterpret_cast<const uint4 *>(a.q + (((size_t)b * a.n + t) * a.Hq + h * a.G + gq) * kHeadDim) + c);
+        }
+        *reinterpret_cast<uint4 *>(sm + (row / kTileR) * kStageBytes + (c >> 3) * kBlkBytes +
+                                   tc::sw_chunk(row % kTileR, c & 7)) = v;
+    }
+    tc::fence_async_smem();
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = s_tmem;
+    volatile int *abort_flag = &s_abort;
+    auto wait = [&](uint64_t *bar, int parity, int code) {
+        if (mbar_wait(bar, (uint32_t)parity, abort_flag)) return true;
+        *abort_flag = 1;
+        atomicExch(a.err, code);
+        return false;
+    };
+
+    if (warp == 4 * QT) {
+        // ------------------------------------------------------- TMA
+        if (lane == 0) {
+            int it = 0;
+            for (; it < 2 * nt; it++) {   // K and V tiles in turn
+                const int s = it % NS;
+                if (it >= NS && !wait(&bar_empty[s], (it / NS - 1) & 1, 31)) break;
+                const int tok = runs.token(j0 + (it >> 1));
+                const CUtensorMap *map = (it & 1) ? &map_v : &map_k;
+                const uint32_t dst = sstage + s * kStageBytes;
+                expect_tx(&bar_full[s], kStageBytes);
+                tma_3d(dst, map, 0, tok, b * a.H + h, &bar_full[s]);
+                tma_3d(dst + kBlkBytes, map, 64, tok, b * a.H + h, &bar_full[s]);
+            }
+            // every issued load must have landed before the CTA exits
+            for (int i = max(0, it - NS); i < it; i++) mbar_wait<256>(&bar_full[i % NS], (i / NS) & 1, abort_flag);
+        }
+        __syncwarp();
+    } else if (warp == 4 * QT + 1) {
+        // ------------------------------------------------------- MMA
+        if (lane == 0) {
+            constexpr uint32_t idS = tc::idesc_bf16(kTileR, kTileT, false);   // K: K-major
+            constexpr uint32_t idO = tc::idesc_bf16(kTileR, kHeadDim, true);  // V: MN-major
+            auto logits = [&](int q, int j) {
+                const int s = (2 * j) % NS;
+                const uint64_t da = tc::desc_k(sbase + q * kStageBytes), db = tc::desc_k(sstage + s * kStageBytes);
+#pragma unroll
+                for (int kk = 0; kk < 8; kk++) {
+                    const uint64_t o = (uint64_t)(((kk >> 2) * kBlkBytes + (kk & 3) * 32) >> 4);
+                    tc::mma_bf16(tmem + q * 256, da + o, db + o, idS, kk > 0);
+                }
+                tc::commit(&bar_sfull[q]);
+                if (q == QT - 1) tc::commit(&bar_empty[s]);
+            };
+            auto values = [&](int q, int j) {
+                const int s = (2 * j + 1) % NS;
+                const uint64_t dv = tc::desc_mn(sstage + s * kStageBytes, kBlkBytes);
+#pragma unroll
+                for (int part = 0; part < (SPLIT ? 2 : 1); part++)
+#pragma unroll
+                    for (int kk = 0; kk < 8; kk++)
+                        mma_ts(tmem + q * 256 + 128, tmem + q * 256 + part * 64 + kk * 8, dv + (uint64_t)((kk * 2048) >> 4),
+                               idO, j > 0 || part > 0 || kk > 0);
+                if (q == QT - 1) tc::commit(&bar_empty[s]);
+                if (j == nt - 1) tc::commit(&bar_ofull[q]);
+            };
+            bool ok = nt == 0 || wait(&bar_full[0], 0, 32);
+            if (nt > 0 && ok) {
+                tc::fence_after();
+                for (int q = 0; q < QT; q++) logits(q, 0);
+            }
+            for (int j = 0; j < nt && ok; j++) {
+                ok = wait(&bar_full[(2 * j + 1) % NS], ((2 * j + 1) / NS) & 1, 33);
+                for (int q = 0; q < QT && ok; q++) {
+                    ok = wait(&bar_pfull[q], j & 1, 34);
+                    if (!ok) break;
+                    tc::fence_after();
+                    values(q, j);
+                    if (j + 1 < nt) {
+                        if (q == 0) ok = wait(&bar_full[(2 * j + 2) % NS], ((2 * j + 2) / NS) & 1, 35);
+                        if (!ok) break;
+                        logits(q, j + 1);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------- softmax
+        const int q = warp >> 2;                       // row tile
+        const int row = q * kTileR + (warp & 3) * 32 + lane;
+        const bool live = q * kTileR + (warp & 3) * 32 < nr;   // warp-uniform: some row of the warp exists
+        const int pos = Tb - a.n + (r0 + row) / a.G;   // the row's position
+        const int lim = pos + 1;
+        const int lo = (int)max(0ll, (long long)pos + 1 - a.window);
+        const uint32_t tS = tmem + q * 256 + ((uint32_t)(32 * (warp & 3)) << 16), tO = tS + 128;
+        const bool careful = __ldcg(a.nonfinite) != 0;
+        float m_used = -CUDART_INF_F, l = 0.f;
+        for (int j = 0; j < nt; j++) {
+            const int tb = runs.token(j0 + j);
+            // a sinks' tile may reach into the window's: its part ends where that begins
+            const int end = j0 + j < runs.sink_tiles ? min(lim, runs.w_tile) : lim;
+            if (careful) {
+                // V rows that are not finite become zeros with a flag (thread t: token t)
+                asm volatile("bar.sync 1, %0;" ::"n"(128 * QT) : "memory");
+                if (q == 0) {
+                    const int s = (2 * j + 1) % NS, t = tid;
+                    wait(&bar_full[s], ((2 * j + 1) / NS) & 1, 36);
+                    uint32_t bad = 0;
+                    for (int c = 0; c < 16; c++) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(stages + s * kStageBytes + (c >> 3) * kBlkBytes +
+                                                                         t * 128 + (c & 7) * 16);
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int i = 0; i < 4; i++) bad |= ((w[i] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+                    }
+                    if (bad)
+                        for (int c = 0; c < 16; c++)
+                            *reinterpret_cast<uint4 *>(stages + s * kStageBytes + (c >> 3) * kBlkBytes + t * 128 +
+                                                       (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    s_bad[t] = bad ? 1 : 0;
+                    tc::fence_async_smem();
+                }
+                asm volatile("bar.sync 1, %0;" ::"n"(128 * QT) : "memory");
+            }
+            wait(&bar_sfull[q], j & 1, 37);
+            tc::fence_after();
+            if (live) {
+                uint32_t s[128];
+#pragma unroll
+                for (int c = 0; c < 4; c++) ld32(tS + 32 * c, s + 32 * c);
+                wait_ld32(s);
+#pragma unroll
+                for (int c = 1; c < 4; c++) settle32(s + 32 * c);
+                if (tb + kTileT > end || (tb < lo && tb + kTileT > a.sinks)) {   // an edge lies in the tile
+#pragma unroll
+                    for (int c = 0; c < 4; c++) {
+                        const int p = tb + 32 * c;
+                        const uint32_t vis = range_bits(0, end - p) & (range_bits(lo - p, 32) | range_bits(0, a.sinks - p));
+#pragma unroll
+                        for (int k = 0; k < 32; k++)
+                            if (!((vis >> k) & 1u)) s[32 * c + k] = 0xFF800000u;   // -inf
+                    }
+                }
+                float mx = __uint_as_float(s[0]);
+#pragma unroll
+                for (int k = 1; k < 128; k++) mx = fmaxf(mx, __uint_as_float(s[k]));
+                mx *= a.scale_log2;
+                const bool raise = mx > m_used + kRaiseLog2;   // false while nothing is seen
+                const bool rescale = raise && m_used != -CUDART_INF_F;
+                const float f = rescale ? exp2f(m_used - mx) : 1.f;
+                if (raise) m_used = mx;
+                if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll 1
+                    for (int c = 0; c < 4; c++) {
+                        uint32_t v[32];
+                        ld32(tO + 32 * c, v);
+                        wait_ld32(v);
+#pragma unroll
+                        for (int k = 0; k < 32; k++) v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
+                        st32(tO + 32 * c, v);
+                    }
+                }
+                l *= f;
+                const float off = m_used == -CUDART_INF_F ? 0.f : -m_used;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < 2; c++) {
+                    uint32_t hi[32], low[32];
+#pragma unroll
+                    for (int k = 0; k < 32; k++) {
+                        const int u = 64 * c + 2 * k;
+                        float p0 = ex2f(fmaf(__uint_as_float(s[u]), a.scale_log2, off));
+                        float p1 = ex2f(fmaf(__uint_as_float(s[u + 1]), a.scale_log2, off));
+                        sum[k & 3] += p0 + p1;
+                        if (careful) {
+                            if (s_bad[u] && p0 != 0.f) p0 = CUDART_NAN_F;
+                            if (s_bad[u + 1] && p1 != 0.f) p1 = CUDART_NAN_F;
+                        }
+                        hi[k] = pack_bf16(p0, p1);
+                        if (SPLIT)
+                            low[k] = pack_bf16(p0 - __uint_as_float(hi[k] << 16), p1 - __uint_as_float(hi[k] & 0xFFFF0000u));
+                    }
+                    __syncwarp();
+                    st32(tS + 32 * c, hi);
+                    if (SPLIT) st32(tS + 64 + 32 * c, low);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tc::wait_st();
+            }
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar_pfull[q]);
+        }
+        // ------------------------------------------------------- output
+        if (nt > 0) {
+            wait(&bar_ofull[q], 0, 38);
+            tc::fence_after();
+        }
+        if (live) {
+            const int rg = r0 + row, t = rg / a.G, gq = rg % a.G;
+            const size_t prow = ((size_t)b * a.n + t) * a.Hq + h * a.G + gq;
+            float *part = a.partials + (prow * a.S + split) * kPartialStride;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+            for (int c = 0; c < 4; c++) {
+                uint32_t v[32];
+                if (nt > 0) {
+                    ld32(tO + 32 * c, v);
+                    wait_ld32(v);
+                }
+                if (row < nr) {
+                    if (nt == 0 || l == 0.f) {
+#pragma unroll
+                        for (int k = 0; k < 32; k++) v[k] = 0u;
+                    }
+                    if (a.S > 1) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4)
+                            *reinterpret_cast<uint4 *>(part + 32 * c + k) = make_uint4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                    } else if (a.out16) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 8) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int i = 0; i < 4; i++)
+                                w[i] = pack_bf16(__uint_as_float(v[k + 2 * i]) * inv, __uint_as_float(v[k + 2 * i + 1]) * inv);
+                            *reinterpret_cast<uint4 *>(a.out16 + prow * kHeadDim + 32 * c + k) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4)
+                            *reinterpret_cast<float4 *>(a.out + prow * kHeadDim + 32 * c + k) =
+                                make_float4(__uint_as_float(v[k]) * inv, __uint_as_float(v[k + 1]) * inv,
+                                            __uint_as_float(v[k + 2]) * inv, __uint_as_float(v[k + 3]) * inv);
+                    }
+                }
+                __syncwarp();   // converged for the next load
+            }
+            if (a.S > 1 && row < nr) {
+                part[kHeadDim] = l == 0.f ? -CUDART_INF_F : m_used;
+                part[kHeadDim + 1] = l;
+            }
+        }
+    }
+    tc::fence_before();
+    __syncthreads();
+    if (warp == 4 * QT + 1) {
+        tc::fence_after();
+        tc::dealloc(tmem, C::COLS);
+    }
+    // ----------------------------------------------------------- split merge
+    // The last split of the row block to arrive merges every split's partial
+    // of its rows; it leaves the counter at zero for the next launch.
+    if (a.S > 1) {
+        __threadfence();
+        __syncthreads();
+        const int unit = (b * a.H + h) * a.nqb + qb;
+        if (tid == 0) s_last = atomicAdd(a.counters + unit, 1) == a.S - 1;
+        __syncthreads();
+        if (!s_last) return;
+        __threadfence();
+        for (int row = warp; row < nr; row += C::THREADS / 32) {
+            const int rg = r0 + row, t = rg / a.G, gq = rg % a.G;
+            const size_t prow = ((size_t)b * a.n + t) * a.Hq + h * a.G + gq;
+            const float *part = a.partials + prow * a.S * kPartialStride;
+            float M = -CUDART_INF_F, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int sp = 0; sp < a.S; sp++) {
+                const float *p = part + (size_t)sp * kPartialStride;
+                const float m = __ldcg(p + kHeadDim), ls = __ldcg(p + kHeadDim + 1);
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(p) + lane);
+                if (m == -CUDART_INF_F && ls == 0.f) continue;   // uniform over the warp: no key in this split
+                const float Mn = fmaxf(M, m);
+                const float c0 = M == -CUDART_INF_F ? 0.f : exp2f(M - Mn), c = m == -CUDART_INF_F ? 1.f : exp2f(m - Mn);
+                l = fmaf(ls, c, l * c0);
+                o[0] = fmaf(v.x, c, o[0] * c0);
+                o[1] = fmaf(v.y, c, o[1] * c0);
+                o[2] = fmaf(v.z, c, o[2] * c0);
+                o[3] = fmaf(v.w, c, o[3] * c0);
+                M = Mn;
+            }
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            if (a.out16)
+                *reinterpret_cast<uint2 *>(a.out16 + prow * kHeadDim + 4 * lane) =
+                    make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
+            else
+                *reinterpret_cast<float4 *>(a.out + prow * kHeadDim + 4 * lane) =
+                    make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+        }
+        if (tid == 0) a.counters[unit] = 0;
+    }
+}
+
+// cuTensorMapEncodeTiled through the runtime (the library links no libcuda).
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                              const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn encode_fn() {
+    static EncodeFn fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            p = nullptr;
+        }
+        return reinterpret_cast<EncodeFn>(p);
+    }();
+    return fn;
+}
+
+// K or V of a BF16 cache, [B * H][Tp][128]: boxes of 128 tokens x 64 elements,
+// 128-byte swizzled; rows past Tp read as zeros.
+bool make_map(CUtensorMap *map, const uint16_t *base, int Tp, long long heads) {
+    const EncodeFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)Tp, (cuuint64_t)heads};
+    const cuuint64_t strides[2] = {kHeadDim * 2, (cuuint64_t)Tp * kHeadDim * 2};
+    const cuuint32_t box[3] = {64, kTileT, 1}, step[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t *>(base), dims, strides, box, step,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int QT, bool SPLIT>
+cudaError_t launch_t(const CUtensorMap &mk, const CUtensorMap &mv, const Bf16Args &a, cudaStream_t st) {
+    static bool done[kMaxDevices];
+    cudaError_t e = once_per_device(done, [] {
+        return cudaFuncSetAttribute(prefill_bf16_kernel<QT, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<QT>::SMEM);
+    });
+    if (e != cudaSuccess) return e;
+    prefill_bf16_kernel<QT, SPLIT><<<dim3(a.S, a.H, a.B * a.nqb), Cfg<QT>::THREADS, Cfg<QT>::SMEM, st>>>(mk, mv, a);
+    return cudaGetLastError();
+}
+
+// Row tiles per CTA: two share their K and V tiles; one while there are no
+// more rows, or too few row blocks to fill the device with pairs.
+int row_tiles(const PrefillArgs &a, int sms) {
+    const long rows = (long)a.n * a.G, units = (long)a.B * a.H;
+    return rows <= kTileR || units * ((rows + 2 * kTileR - 1) / (2 * kTileR)) < sms ? 1 : 2;
+}
+
+}  // namespace
+
+void prefill_bf16_plan(PrefillArgs *a, int sms) {
+    const int rows = kTileR * row_tiles(*a, sms), slots = sms * (rows == kTileR ? Cfg<1>::CTAS : Cfg<2>::CTAS);
+    const int nq = a->n * a->G;
+    a->nqb = (nq + rows - 1) / rows;
+    // tiles of all row blocks, and of the longest
+    long total = 0;
+    int nt = 1;
+    for (int b = 0; b < a->B; b++)
+        for (int r0 = 0; r0 < nq; r0 += rows) {
+            const int t = Runs(a->seqT.v[b], a->n, r0 / a->G, (std::min(r0 + rows, nq) - 1) / a->G, a->window, a->sinks).tiles;
+            total += t;
+            nt = std::max(nt, t);
+        }
+    total *= a->H;
+    // In tiles' time: the work of all CTAs (set-up and output about two tiles
+    // each, the partials of a split another two) over the slots, and half of
+    // the longest CTA for the uneven end.
+    const long units = (long)a->B * a->H * a->nqb;
+    double best = -1;
+    for (int S = 1; S <= std::min(nt, kMaxSplits); S++) {
+        const int fixed = S > 1 ? 4 : 2;
+        const double longest = (nt + S - 1) / S + fixed;
+        const double cost = std::max((total + (double)units * S * fixed) / slots + 0.5 * longest, longest);
+        if (best < 0 || cost < best) {
+            best = cost;
+            a->S = S;
+        }
+    }
+}
+
+cudaError_t launch_prefill_bf16(const PrefillArgs &p, const uint16_t *k, const uint16_t *v, const int *nonfinite, int sms,
+                                cudaStream_t st) {
+    CUtensorMap mk, mv;
+    const long long heads = (long long)p.B * p.H;
+    if (!make_map(&mk, k, p.Tp, heads) || !make_map(&mv, v, p.Tp, heads)) return cudaErrorInvalidValue;
+    Bf16Args a;
+    a.q = p.q;
+    a.partials = p.partials;
+    a.out = p.out;
+    a.out16 = p.out16;
+    a.counters = p.counters;
+    a.err = p.err;
+    a.nonfinite = nonfinite;
+    a.seqT = p.seqT;
+    a.B = p.B;
+    a.H = p.H;
+    a.Hq = p.Hq;
+    a.G = p.G;
+    a.n = p.n;
+    a.S = p.S;
+    a.nqb = p.nqb;
+    a.window = p.window;
+    a.sinks = p.sinks;
+    a.scale_log2 = p.scale_log2;
+    if (row_tiles(p, sms) == 1) return p.out16 ? launch_t<1, false>(mk, mv, a, st) : launch_t<1, true>(mk, mv, a, st);
+    return p.out16 ? launch_t<2, false>(mk, mv, a, st) : launch_t<2, true>(mk, mv, a, st);
+}
+
+}  // namespace rq

@@ -93,7 +93,7 @@ struct Layout {
     size_t records_bytes;
     size_t off_partials;         // float [B][Hq][splits_max][kPartialStride]
     size_t off_counters;         // int [B][H_kv]
-    size_t off_err;              // int error word (+ pad)
+    size_t off_err;              // int error word; the next int: a V that is not finite was ever stored (BF16 format)
     size_t off_vmax;             // int [layers][groups][Lg][B][H_kv]: largest V scale byte per stream
     size_t off_table;            // int [B][MB]: block table (paged)
     size_t total;
@@ -145,6 +145,7 @@ struct Bf16StoreArgs {
     const uint16_t *src[2];   // [B][n][H][d]
     uint16_t *dst[2];         // [B][H][Tp][d]
     SeqLens pos0;             // first token position written, per sequence
+    int *nonfinite;           // set to 1 when a V value is not finite
     int B, H, n, Tp;
 };
 

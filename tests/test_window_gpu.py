@@ -451,3 +451,106 @@ def test_prefill_window_refusals():
         assert e.value.status == rq.RQ_ERR_UNSUPPORTED
         other.cache.close()
     bt.cache.close()
+
+
+# ------------------------------------------------------------------ several tokens over a BF16 cache
+def _bf16(T, B=1, H_=2, Hq=2, lens=None, seed=0x5EEDDD01):
+    bt = H.build(loops=1, Lg=1, B=B, T=T, H=H_, Hq=Hq, fmt=rq.RQ_FMT_BF16, seed=seed, max_tokens=T + 3)
+    for b, n in enumerate(lens or []):
+        bt.cache.truncate_seq(0, 0, b, n)
+    return bt, lens or [T] * B
+
+
+# fp32 output: weights to 2^-17 relative (BF16 pairs), 2^-22 exponentials, fp32 sums: 1e-5 of the row; BF16 output:
+# weights to half a BF16 step, 2^-9 (at random over the tokens: of the row's norm; at most 2^-9 max|v|, |v| < 45), on top of
+# the output's own half step
+@pytest.mark.parametrize("T,n", [(1, 1), (5, 5), (127, 3), (128, 128), (129, 129), (257, 130), (640, 65), (1000, 700)])
+@pytest.mark.parametrize("Hq", [2, 8, 16])
+def test_prefill_windows_of_a_bf16_cache(T, n, Hq):
+    bt, lens = _bf16(T, Hq=Hq)
+    for window, sinks in ((0, 0), (1, 0), (5, 2), (64, 4), (128, 0), (200, 150), (BIG, 3)):
+        chunk_check(bt, 0, lens, n, window, sinks, torch.float32, rel=1e-5, mx=2e-4)
+        chunk_check(bt, 0, lens, n, window, sinks, torch.bfloat16, rel=2.0 ** -9, mx=9e-2)
+    bt.cache.check()
+    bt.cache.close()
+
+
+def test_prefill_windows_of_ragged_bf16_sequences():
+    bt, lens = _bf16(1500, B=4, Hq=4, lens=[1500, 70, 300, 129])
+    for n in (1, 33, 70):
+        for window, sinks in ((0, 0), (1, 1), (64, 4), (257, 130), (1000, 0)):
+            chunk_check(bt, 0, lens, n, window, sinks, rel=1e-5, mx=2e-4)
+    bt.cache.check()
+    bt.cache.close()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+def test_prefill_of_a_long_bf16_chunk(dtype):
+    """Enough rows for two row tiles a CTA: the whole prompt, and a window with sinks."""
+    bt, lens = _bf16(2300, B=1, H_=16, Hq=32)
+    tol = dict(rel=1e-5, mx=2e-4) if dtype == torch.float32 else dict(rel=2.0 ** -9, mx=9e-2)
+    chunk_check(bt, 0, lens, 2300, 0, 0, dtype, **tol)
+    chunk_check(bt, 0, lens, 2201, 300, 20, dtype, **tol)
+    bt.cache.check()
+    bt.cache.close()
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("n", [80, 600])
+def test_bf16_prefill_does_not_see_what_masked_tokens_hold(value, n):
+    T, at = 700, 650
+    bt, lens = _bf16(T, H_=16, Hq=16 if n == 80 else 32)
+    K, V = bt.inputs[(0, 0)]
+    kv0 = keys_values(bt, 0, 0, lens)
+    bt.cache.truncate(0, 0, 0)
+    K, V = ([X[0].clone()] for X in (K, V))
+    for X in (K, V):
+        X[0][:, at] = value
+        X[0][:, 3:40] = value                # beside the sinks, far outside every window
+    bt.cache.append(0, 0, K[0].contiguous(), V[0].contiguous())
+    q = queries(15, 1, n, bt.cfg.num_q_heads, 128)
+    window, sinks = 40, 3
+    ref = reference(kv0, q, window, sinks)
+    pos = np.arange(T - n, T)
+    blind = (at > pos) | (at <= pos - window)
+    for dtype, tol in ((torch.float32, 1e-5), (torch.bfloat16, 2.0 ** -8)):
+        got = bt.cache.prefill_window(0, 0, q, window, sinks, dtype=dtype).double().cpu().numpy()
+        rows = blind & (pos >= 40 + window)      # those that also see none of 3 .. 39
+        assert rows.any() and np.isfinite(got[:, rows]).all()
+        assert np.linalg.norm(got[:, rows] - ref[:, rows]) <= tol * np.linalg.norm(ref[:, rows])
+        if np.isnan(value):
+            assert np.isnan(got[:, ~blind]).all()
+    bt.cache.check()
+    bt.cache.close()
+
+
+def test_bf16_prefill_repeats_itself():
+    bt, lens = _bf16(1500, B=2, Hq=4, lens=[1500, 900])
+    q = queries(16, 2, 33, 4, 128)
+    first = bt.cache.prefill_window(0, 0, q, 700, 4)
+    one = bt.cache.prefill_window(0, 0, q[:, -1:].contiguous(), 700, 4)
+    check(one, bt.cache.decode_window(0, 0, q[:, -1].contiguous(), 700, 4)[:, None].double().cpu().numpy(), 1e-5, 2e-4)
+    out = torch.zeros_like(first)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        with pytest.raises(rq.RQError) as e:           # more splits than any call so far: no room, and none while capturing
+            bt.cache.prefill_window(0, 0, q, 0)
+        assert e.value.status == rq.RQ_ERR_NOMEM
+        bt.cache.prefill_window(0, 0, q, 700, 4, out=out)
+    g.replay()
+    assert torch.equal(out, first)
+    bt.cache.prefill_window(0, 0, q, 0)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        bt.cache.prefill_window(0, 0, q, 0)
+        bt.cache.prefill_window(0, 0, q, 700, 4, out=out)
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        assert torch.equal(out, first)
+        assert torch.equal(bt.cache.prefill_window(0, 0, q, 700, 4), first)
+    with pytest.raises(rq.RQError) as e:
+        bt.cache.prefill(0, 0, q)
+    assert e.value.status == rq.RQ_ERR_STATE
+    bt.cache.check()
+    bt.cache.close()
