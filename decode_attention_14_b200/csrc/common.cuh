@@ -27,6 +27,32 @@ __device__ __forceinline__ uint32_t f64_to_e4m3(double v) {
 // Sign bit j of the seeded diagonal sigma (1 -> multiply by -1).
 __device__ __forceinline__ bool sigma_neg(const uint32_t sigma[4], int j) { return (sigma[j >> 5] >> (j & 31)) & 1u; }
 
+// Two fp32 operations per instruction.
+struct F2 {
+    unsigned long long v;
+};
+__device__ __forceinline__ F2 pack2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(F2 p, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p.v)); }
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
 // In-warp fast Walsh-Hadamard transform of a 128-vector held as 4
 // consecutive elements per lane (element 4*lane + k in v[k]); computes
 // H_128 v in Sylvester (natural) order, unnormalised.

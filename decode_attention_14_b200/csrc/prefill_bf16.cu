@@ -359,9 +359,14 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, Cfg<QT>::CTAS)
                             if (!((vis >> k) & 1u)) s[32 * c + k] = 0xFF800000u;   // -inf
                     }
                 }
-                float mx = __uint_as_float(s[0]);
+                float m8[8];   // independent chains: one would be 127 dependent steps
 #pragma unroll
-                for (int k = 1; k < 128; k++) mx = fmaxf(mx, __uint_as_float(s[k]));
+                for (int k = 0; k < 8; k++) m8[k] = __uint_as_float(s[k]);
+#pragma unroll
+                for (int k = 8; k < 128; k += 8)
+#pragma unroll
+                    for (int i = 0; i < 8; i++) m8[i] = fmaxf(m8[i], __uint_as_float(s[k + i]));
+                float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])), fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
                 mx *= a.scale_log2;
                 const bool raise = mx > m_used + kRaiseLog2;   // false while nothing is seen
                 const bool rescale = raise && m_used != -CUDART_INF_F;
@@ -380,20 +385,32 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, Cfg<QT>::CTAS)
                 }
                 l *= f;
                 const float off = m_used == -CUDART_INF_F ? 0.f : -m_used;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const F2 sc2 = pack2(a.scale_log2, a.scale_log2), off2 = pack2(off, off);
+                F2 sum[4];
+#pragma unroll
+                for (int k = 0; k < 4; k++) sum[k] = pack2(0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < 128; k += 2) {
+                    float p0, p1;
+                    unpack2(fma2(pack2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), sc2, off2), p0, p1);
+                    p0 = ex2f(p0);
+                    p1 = ex2f(p1);
+                    sum[(k / 2) & 3] = add2(sum[(k / 2) & 3], pack2(p0, p1));
+                    s[k] = __float_as_uint(p0);
+                    s[k + 1] = __float_as_uint(p1);
+                }
+                if (careful) {
+#pragma unroll
+                    for (int k = 0; k < 128; k++)
+                        if (s_bad[k] && __uint_as_float(s[k]) != 0.f) s[k] = 0x7FC00000u;   // NaN
+                }
 #pragma unroll
                 for (int c = 0; c < 2; c++) {
                     uint32_t hi[32], low[32];
 #pragma unroll
                     for (int k = 0; k < 32; k++) {
                         const int u = 64 * c + 2 * k;
-                        float p0 = ex2f(fmaf(__uint_as_float(s[u]), a.scale_log2, off));
-                        float p1 = ex2f(fmaf(__uint_as_float(s[u + 1]), a.scale_log2, off));
-                        sum[k & 3] += p0 + p1;
-                        if (careful) {
-                            if (s_bad[u] && p0 != 0.f) p0 = CUDART_NAN_F;
-                            if (s_bad[u + 1] && p1 != 0.f) p1 = CUDART_NAN_F;
-                        }
+                        const float p0 = __uint_as_float(s[u]), p1 = __uint_as_float(s[u + 1]);
                         hi[k] = pack_bf16(p0, p1);
                         if (SPLIT)
                             low[k] = pack_bf16(p0 - __uint_as_float(hi[k] << 16), p1 - __uint_as_float(hi[k] & 0xFFFF0000u));
@@ -402,7 +419,9 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, Cfg<QT>::CTAS)
                     st32(tS + 32 * c, hi);
                     if (SPLIT) st32(tS + 64 + 32 * c, low);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                float l0, l1;
+                unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), l0, l1);
+                l += l0 + l1;
                 tc::wait_st();
             }
             tc::fence_before();
