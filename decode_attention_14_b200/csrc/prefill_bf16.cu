@@ -359,6 +359,11 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, Cfg<QT>::CTAS)
                             if (!((vis >> k) & 1u)) s[32 * c + k] = 0xFF800000u;   // -inf
                     }
                 }
+                if (careful) {   // a visible token whose V is not finite
+#pragma unroll
+                    for (int k = 0; k < 128; k++)
+                        if (s_bad[k] && s[k] != 0xFF800000u) s[k] = 0x7FC00000u;   // NaN
+                }
                 float m8[8];   // independent chains: one would be 127 dependent steps
 #pragma unroll
                 for (int k = 0; k < 8; k++) m8[k] = __uint_as_float(s[k]);
@@ -390,27 +395,16 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, Cfg<QT>::CTAS)
 #pragma unroll
                 for (int k = 0; k < 4; k++) sum[k] = pack2(0.f, 0.f);
 #pragma unroll
-                for (int k = 0; k < 128; k += 2) {
-                    float p0, p1;
-                    unpack2(fma2(pack2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), sc2, off2), p0, p1);
-                    p0 = ex2f(p0);
-                    p1 = ex2f(p1);
-                    sum[(k / 2) & 3] = add2(sum[(k / 2) & 3], pack2(p0, p1));
-                    s[k] = __float_as_uint(p0);
-                    s[k + 1] = __float_as_uint(p1);
-                }
-                if (careful) {
-#pragma unroll
-                    for (int k = 0; k < 128; k++)
-                        if (s_bad[k] && __uint_as_float(s[k]) != 0.f) s[k] = 0x7FC00000u;   // NaN
-                }
-#pragma unroll
                 for (int c = 0; c < 2; c++) {
                     uint32_t hi[32], low[32];
 #pragma unroll
                     for (int k = 0; k < 32; k++) {
                         const int u = 64 * c + 2 * k;
-                        const float p0 = __uint_as_float(s[u]), p1 = __uint_as_float(s[u + 1]);
+                        float p0, p1;
+                        unpack2(fma2(pack2(__uint_as_float(s[u]), __uint_as_float(s[u + 1])), sc2, off2), p0, p1);
+                        p0 = ex2f(p0);
+                        p1 = ex2f(p1);
+                        sum[k & 3] = add2(sum[k & 3], pack2(p0, p1));
                         hi[k] = pack_bf16(p0, p1);
                         if (SPLIT)
                             low[k] = pack_bf16(p0 - __uint_as_float(hi[k] << 16), p1 - __uint_as_float(hi[k] & 0xFFFF0000u));
