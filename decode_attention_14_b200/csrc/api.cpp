@@ -40,6 +40,9 @@ struct rq_cache {
     // launch leaves them at zero)
     int *prefill_cnt = nullptr;
     size_t prefill_cnt_n = 0;
+    // rebuilt rows of rq_prefill_attn_window's long chunks, likewise
+    uint16_t *rebuild_ws = nullptr;
+    size_t rebuild_bytes = 0;
     // paged records: host copy of the block table [B][MB] (-1: no block),
     // reference counts of the physical blocks (forked sequences share
     // blocks), and the free list (blocks are taken from its back)
@@ -577,12 +580,13 @@ int rq_cache_create(const rq_config *cfg, void *dev_mem, size_t bytes, rq_cache 
 int rq_cache_destroy(rq_cache *c) {
     if (!c) return RQ_OK;
     int st = RQ_OK;
-    if (c->owned || c->prefill_ws || c->prefill_cnt) {
+    if (c->owned || c->prefill_ws || c->prefill_cnt || c->rebuild_ws) {
         if (cudaDeviceSynchronize() != cudaSuccess) st = RQ_ERR_CUDA;
     }
     if (c->owned) cudaFree(c->base);
     if (c->prefill_ws) cudaFree(c->prefill_ws);
     if (c->prefill_cnt) cudaFree(c->prefill_cnt);
+    if (c->rebuild_ws) cudaFree(c->rebuild_ws);
     delete c;
     return st;
 }
@@ -890,16 +894,23 @@ int rq_decode_attn_window(rq_cache *c, int layer, int loop, const void *q, void 
 
 namespace {
 
+// bytes of rebuilt rows a call keeps at once (more only if one kv head's rows are)
+#ifndef RQ_REBUILD_MAX
+#define RQ_REBUILD_MAX (size_t(4) << 30)
+#endif
+constexpr size_t kRebuildMax = RQ_REBUILD_MAX;
+
+bool capturing(cudaStream_t st) {
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    return st && cudaStreamIsCapturing(st, &cap) == cudaSuccess && cap != cudaStreamCaptureStatusNone;
+}
+
 // Room for `floats` split partials and `units` arrival counters of the
 // multi-token attention, kept by the cache and grown on demand.
 // While `st` is being captured nothing can be allocated: NOMEM, the capture
 // left valid.
 int prefill_workspace(rq_cache *c, size_t floats, size_t units, cudaStream_t st) {
-    if (st && (floats > c->prefill_ws_floats || units > c->prefill_cnt_n)) {
-        cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-        if (cudaStreamIsCapturing(st, &cap) != cudaSuccess) return RQ_ERR_CUDA;
-        if (cap != cudaStreamCaptureStatusNone) return RQ_ERR_NOMEM;
-    }
+    if ((floats > c->prefill_ws_floats || units > c->prefill_cnt_n) && capturing(st)) return RQ_ERR_NOMEM;
     if (floats > c->prefill_ws_floats) {
         if (c->prefill_ws) {
             if (cudaDeviceSynchronize() != cudaSuccess) return RQ_ERR_CUDA;
@@ -934,6 +945,68 @@ int prefill_workspace(rq_cache *c, size_t floats, size_t units, cudaStream_t st)
         c->prefill_cnt = (int *)p;
         c->prefill_cnt_n = units;
     }
+    return RQ_OK;
+}
+
+// The first launch of a windowed chunk over the compressed cache (rebuild.cu):
+// the rows that the chunk sees, for as many kv heads at a time (r->H) as a
+// workspace of kRebuildMax holds, at least one.
+int plan_rebuild(rq_cache *c, const PrefillArgs &a, cudaStream_t st, ReadArgs *r) {
+    int rows = 0;
+    for (int b = 0; b < a.B; b++)
+        rows = std::max(rows, rebuilt_rows(a.seqT.v[b], a.n_tail, a.n, a.window, a.sinks).rows(a.seqT.v[b]));
+    rows = (rows + 15) / 16 * 16 + 128;   // a reader's tile may begin at the last row
+    const size_t head = (size_t)a.B * rows * kHeadDim;   // elements of one part of one kv head
+    const int parts = a.out16 ? 3 : 4;                   // K high and low, V (high and low)
+    const int heads = (int)std::min<size_t>(a.H, std::max<size_t>(1, kRebuildMax / (head * 2 * parts)));
+    const size_t part = head * heads;
+    if (part * 2 * parts > c->rebuild_bytes) {
+        if (capturing(st)) return RQ_ERR_NOMEM;
+        if (c->rebuild_ws) {
+            if (cudaDeviceSynchronize() != cudaSuccess) return RQ_ERR_CUDA;
+            cudaFree(c->rebuild_ws);
+            c->rebuild_ws = nullptr;
+            c->rebuild_bytes = 0;
+        }
+        void *p = nullptr;
+        if (cudaMalloc(&p, part * 2 * parts) != cudaSuccess) {
+            cudaGetLastError();
+            return RQ_ERR_NOMEM;
+        }
+        c->rebuild_ws = (uint16_t *)p;
+        c->rebuild_bytes = part * 2 * parts;
+    }
+    std::memset(r, 0, sizeof(*r));
+    for (int kv = 0; kv < 2; kv++) {
+        r->a_codes[kv] = a.a_codes[kv];
+        r->a_meta[kv] = a.a_meta[kv];
+        r->r_codes[kv] = a.r_codes[kv];
+        r->r_meta[kv] = a.r_meta[kv];
+        r->r_coef[kv] = (const uint8_t *)a.r_coef[kv];
+    }
+    r->nr = a.r_codes[0] ? 1 : 0;
+    r->tail[0] = a.tail_k;
+    r->tail[1] = a.tail_v;
+    r->out[0] = c->rebuild_ws;
+    r->out_lo[0] = c->rebuild_ws + part;
+    r->out[1] = c->rebuild_ws + 2 * part;
+    r->out_lo[1] = parts == 4 ? c->rebuild_ws + 3 * part : nullptr;
+    r->pair_stride = rows;
+    r->pair_rows = rows;
+    r->seqT = a.seqT;
+    r->pg = a.pg;
+    r->B = a.B;
+    r->H = heads;
+    r->H_all = a.H;
+    r->n = a.n;
+    r->n_tail = a.n_tail;
+    r->tail_cap = a.tail_cap;
+    r->g = a.g;
+    r->rotate = a.rotate;
+    std::memcpy(r->sigma, a.sigma, sizeof(r->sigma));
+    r->window = a.window;
+    r->sinks = a.sinks;
+    r->nonfinite = nonfinite_ptr(c);
     return RQ_OK;
 }
 
@@ -989,6 +1062,7 @@ int prefill_common(rq_cache *c, int layer, int loop, const void *q, int n, void 
     a.rotate = cfg.rotate;
     std::memcpy(a.sigma, &c->sigma[(size_t)layer * 4], sizeof(a.sigma));
     if (n > 65535) return RQ_ERR_UNSUPPORTED;   // grid limit
+    ReadArgs rd = {};
     if (win) {
         a.window = win->window;
         a.sinks = win->sinks;
@@ -996,24 +1070,38 @@ int prefill_common(rq_cache *c, int layer, int loop, const void *q, int n, void 
             a.out16 = (uint16_t *)out;
             a.out = nullptr;
         }
-        if (bf16) prefill_bf16_plan(&a, c->sms);
-        else prefill_window_plan(&a, c->sms);
+        prefill_bf16_plan(&a, c->sms);
     } else {
         prefill_plan(&a, T, cfg.anchor_bits, cfg.resid_bits, c->sms);
     }
     if ((long)a.B * a.nqb > 65535) return RQ_ERR_UNSUPPORTED;
-    // a windowed call of one split writes its rows directly
-    const bool direct = win && a.S == 1;
-    const int s = prefill_workspace(c, direct ? 0 : (size_t)a.B * n * a.Hq * std::max(a.S, 1) * kPartialStride,
-                                    direct || a.S == 0 ? 0 : (size_t)a.B * a.H * a.nqb, (cudaStream_t)stream);
+    a.err = (int *)(c->base + L.off_err);
+    cudaStream_t st = (cudaStream_t)stream;
+    const size_t partials = (size_t)a.B * n * a.Hq * std::max(a.S, 1) * kPartialStride;
+    if (!win) {
+        const int s = prefill_workspace(c, partials, a.S > 0 ? (size_t)a.B * a.H * a.nqb : 0, st);
+        if (s != RQ_OK) return s;
+        a.partials = c->prefill_ws;
+        a.counters = a.S > 0 ? c->prefill_cnt : nullptr;
+        return cuda_status(launch_prefill(a, cfg.anchor_bits, cfg.resid_bits, st));
+    }
+    int s = prefill_workspace(c, a.S > 1 ? partials : 0, 0, st);   // one split writes its rows directly
     if (s != RQ_OK) return s;
     a.partials = c->prefill_ws;
-    a.counters = a.S > 0 ? c->prefill_cnt : nullptr;
-    a.err = (int *)(c->base + L.off_err);
-    if (bf16)
-        return cuda_status(launch_prefill_bf16(a, bf16_ptr(c, layer, loop, 0), bf16_ptr(c, layer, loop, 1),
-                                               nonfinite_ptr(c), c->sms, (cudaStream_t)stream));
-    return cuda_status(launch_prefill(a, cfg.anchor_bits, cfg.resid_bits, (cudaStream_t)stream));
+    if (bf16) {
+        s = cuda_status(launch_prefill_bf16(a, bf16_ptr(c, layer, loop, 0), bf16_ptr(c, layer, loop, 1), nonfinite_ptr(c),
+                                            c->sms, st));
+    } else {
+        s = plan_rebuild(c, a, st, &rd);
+        const int heads = rd.H;
+        for (rd.h0 = 0; s == RQ_OK && rd.h0 < a.H; rd.h0 += heads) {
+            rd.H = std::min(heads, a.H - rd.h0);
+            s = cuda_status(launch_rebuild(rd, cfg.anchor_bits, cfg.resid_bits, st));
+            if (s == RQ_OK) s = cuda_status(launch_prefill_rebuilt(a, rd, c->sms, st));
+        }
+    }
+    if (s == RQ_OK && a.S > 1) s = cuda_status(launch_merge_rows(a, st));
+    return s;
 }
 
 }  // namespace

@@ -38,15 +38,11 @@ struct PrefillArgs {
 };
 
 // What the rows of query tokens [i0, i1] of a windowed call see of a sequence
-// of T committed and n_tail tail tokens, as runs that whole 64-token tiles of
-// are read: committed [0, sink_end) and [w_tile, lim) (the first row's window
-// begins at w0), tail tokens [tail0, tail1).  The runs are dealt over the
-// splits as one, the sinks' padded to a tile.
+// of T committed and n_tail tail tokens: committed [0, sink_end) and [w_tile,
+// lim) (the first row's window begins at w0, in the 64 tokens from w_tile on),
+// tail tokens [tail0, tail1).
 struct BlockRuns {
     int sink_end, w_tile, w0, lim, tail0, tail1;
-    __host__ __device__ int sink_pad() const { return (sink_end + kTokTile - 1) / kTokTile * kTokTile; }
-    __host__ __device__ int committed() const { return sink_pad() + (lim - w_tile + kTokTile - 1) / kTokTile * kTokTile; }
-    __host__ __device__ int total() const { return committed() + tail1 - tail0; }
 };
 __host__ __device__ inline BlockRuns block_runs(int T, int n_tail, int n, int i0, int i1, int window, int sinks) {
     BlockRuns r;
@@ -65,16 +61,17 @@ __host__ __device__ inline BlockRuns block_runs(int T, int n_tail, int n, int i0
 // Sets a->nqb and the split count a->S over the committed tokens (T
 // = the longest sequence); a->B, H, G and n must be set.
 void prefill_plan(PrefillArgs *a, int T, int ba, int br, int sms);
-// The same for a windowed call (a->window, a->sinks, a->n_tail and a->seqT set).
-void prefill_window_plan(PrefillArgs *a, int sms);
-cudaError_t launch_prefill_window(const PrefillArgs &a, int ba, int br, cudaStream_t st);
-// a.window > 0: windowed
 cudaError_t launch_prefill(const PrefillArgs &a, int ba, int br, cudaStream_t st);
 
-// Attention of several new tokens over a BF16 cache (prefill_bf16.cu): k, v
-// [B * H][Tp][d]; a->nqb and a->S are the plan's; tail and record fields unused.
+// Windowed attention of several new tokens (prefill_bf16.cu): over a BF16 cache,
+// k, v [B * H][Tp][d]; or over the rows that launch_rebuild wrote as `r` says,
+// then the tail, for the kv heads [r.h0, r.h0 + r.H).  a->nqb and a->S are the
+// plan's; record fields are unused.  With a->S > 1 launch_merge_rows follows.
+struct ReadArgs;
 void prefill_bf16_plan(PrefillArgs *a, int sms);
 cudaError_t launch_prefill_bf16(const PrefillArgs &a, const uint16_t *k, const uint16_t *v, const int *nonfinite, int sms,
                                 cudaStream_t st);
+cudaError_t launch_prefill_rebuilt(const PrefillArgs &a, const ReadArgs &r, int sms, cudaStream_t st);
+cudaError_t launch_merge_rows(const PrefillArgs &a, cudaStream_t st);
 
 }  // namespace rq

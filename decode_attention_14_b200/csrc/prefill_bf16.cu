@@ -20,6 +20,7 @@
 // With QT = 2 one row tile's MMAs run while the other's softmax does, and both
 // share every K and V tile, which halves the L2 traffic (a 128 x 128 tile pair
 // is 64 KB for 2 x 1024 tensor cycles); with QT = 1 two CTAs share an SM.
+// Several splits' partials are merged by a launch of its own.
 //
 // Warps: 4 QT softmax warps (a thread per row: tensor-memory lane = row), then
 // one that issues the TMA loads (K and V tiles alternate in a ring of
@@ -32,6 +33,14 @@
 //   pfull[q]  softmax -> MMA      P of row tile q written
 //   ofull[q]  MMA commit -> softmax   the last values complete
 //
+// RB: the same over a compressed cache.  A first launch (rebuild.cu) writes the
+// committed tokens that the chunk sees as BF16 high and low parts into a
+// workspace, once for all the chunk's rows; then S = Q (Khi + Klo)^T, and for
+// fp32 output O += Phi Vhi + Plo Vhi + Phi Vlo (relative 2^-17).  For BF16
+// output V's low part is left out like P's: both round at random, half a step
+// each.  The tail's tokens are BF16 as they are; their tiles follow the
+// committed ones and have no low parts.
+//
 // A V row that only some rows see may hold NaN or infinities, which 0 * NaN
 // would carry into the other rows.  The store kernel notes in the arena when it
 // was ever given such a V (a.nonfinite); only then, the first softmax warps look
@@ -42,10 +51,12 @@
 #include <math_constants.h>
 
 #include <algorithm>
+#include <cstring>
 
 #include "combine.cuh"
 #include "common.cuh"
 #include "prefill.h"
+#include "read.h"
 #include "sync.cuh"
 #include "tc.cuh"
 
@@ -57,6 +68,7 @@ constexpr int kTileR = 128;                          // rows per row tile
 constexpr int kBlkBytes = 128 * 128;                 // 128 rows of 64 BF16 columns
 constexpr int kStageBytes = 2 * kBlkBytes;           // a K or V tile, or a Q row tile
 constexpr float kRaiseLog2 = 8.f;
+constexpr int kMerge = 8;                            // split partials of a row loaded at once
 
 template <int QT>
 struct Cfg {
@@ -73,6 +85,13 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, int
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
         "[%5];" ::"r"(dst),
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
         : "memory");
 }
 __device__ __forceinline__ void expect_tx(uint64_t *bar, uint32_t bytes) {
@@ -142,39 +161,50 @@ struct Bf16Args {
     float *partials;        // [B][n][Hq][S][kPartialStride]
     float *out;             // [B][n][Hq][d] fp32, or
     uint16_t *out16;        // BF16
-    int *counters;          // [B][H][nqb] split arrivals
     int *err;
     const int *nonfinite;   // a V that is not finite was ever stored
     SeqLens seqT;
-    int B, H, Hq, G, n, S, nqb;
+    int B, H, Hq, G, n, n_tail, S, nqb;
+    int h0;                 // RB: the launch's first kv head; z counts the launch's heads
+    int heads;              // of the launch
     int window, sinks;
     float scale_log2;
 };
 
-// The token runs that rows of query tokens [i0, i1] read, in tiles of 128.
+// Tensor maps: K and V (their high parts under RB), the low parts, the tail's.
+struct Maps {
+    CUtensorMap k, v, k_lo, v_lo, tail_k, tail_v;
+};
+
+// The token runs that rows of query tokens [i0, i1] read, in tiles of 128: the
+// sinks', the window's, the tail's.
 struct Runs {
-    int sink_tiles, w_tile, tiles;
-    __host__ __device__ Runs(int T, int n, int i0, int i1, int window, int sinks) {
-        const BlockRuns r = block_runs(T, 0, n, i0, i1, window, sinks);
+    int sink_tiles, sink_end, w_tile, committed, tail0, tiles;
+    __host__ __device__ Runs(int T, int n_tail, int n, int i0, int i1, int window, int sinks) {
+        const BlockRuns r = block_runs(T, n_tail, n, i0, i1, window, sinks);
         w_tile = r.w_tile;
+        sink_end = r.sink_end;
         sink_tiles = (r.sink_end + kTileT - 1) / kTileT;
-        tiles = sink_tiles + (r.lim - r.w_tile + kTileT - 1) / kTileT;
+        committed = sink_tiles + (r.lim - r.w_tile + kTileT - 1) / kTileT;
+        tail0 = r.tail0;
+        tiles = committed + (r.tail1 - r.tail0 + kTileT - 1) / kTileT;
     }
+    // first committed token of a tile below `committed`, first tail token of one from there on
     __host__ __device__ int token(int tile) const {
-        return tile < sink_tiles ? tile * kTileT : w_tile + (tile - sink_tiles) * kTileT;
+        return tile < sink_tiles ? tile * kTileT
+                                 : tile < committed ? w_tile + (tile - sink_tiles) * kTileT : tail0 + (tile - committed) * kTileT;
     }
 };
 
-template <int QT, bool SPLIT>
+template <int QT, bool SPLIT, bool RB>
 __global__ void __launch_bounds__(Cfg<QT>::THREADS, Cfg<QT>::CTAS)
-    prefill_bf16_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                        const Bf16Args a) {
+    prefill_bf16_kernel(const __grid_constant__ Maps maps, const Bf16Args a) {
     using C = Cfg<QT>;
     constexpr int NS = C::STAGES;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bar_full[NS], bar_empty[NS], bar_sfull[QT], bar_pfull[QT], bar_ofull[QT];
     __shared__ uint32_t s_tmem;
-    __shared__ int s_abort, s_last;
+    __shared__ int s_abort;
     __shared__ uint8_t s_bad[kTileT];
 
     const uint32_t raw_base = smem_u32(smem_raw);
@@ -184,15 +214,21 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, Cfg<QT>::CTAS)
     const uint32_t sstage = sbase + QT * kStageBytes;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int split = blockIdx.x, h = blockIdx.y;
+    const int split = blockIdx.x, h = a.h0 + blockIdx.y, z = blockIdx.z / a.nqb * a.heads + blockIdx.y;
     const int b = blockIdx.z / a.nqb, qb = a.nqb - 1 - blockIdx.z % a.nqb;   // the longest row blocks first
     const int r0 = qb * QT * kTileR;
     const int nr = min(QT * kTileR, a.n * a.G - r0);
     const int Tb = a.seqT.v[b];
-    const Runs runs(Tb, a.n, r0 / a.G, (r0 + nr - 1) / a.G, a.window, a.sinks);
+    const Runs runs(Tb, a.n_tail, a.n, r0 / a.G, (r0 + nr - 1) / a.G, a.window, a.sinks);
     // this split's tiles
     const int j0 = (int)((long long)split * runs.tiles / a.S), j1 = (int)((long long)(split + 1) * runs.tiles / a.S);
     const int nt = j1 - j0;
+    // Stages of tile j of the split: K, V -- or, of a rebuilt tile, K high and
+    // low, V (SPLIT: high and low); kstage / vstage are its first of each.
+    constexpr int CST = SPLIT ? 4 : 3;
+    const int nc = RB ? max(0, min(j1, runs.committed) - j0) : 0;   // rebuilt tiles
+    auto kstage = [&](int j) { return RB ? (j <= nc ? CST * j : CST * nc + 2 * (j - nc)) : 2 * j; };
+    auto vstage = [&](int j) { return kstage(j) + (RB && j < nc ? 2 : 1); };
 
     if (tid == 0) {
         for (int i = 0; i < NS; i++) {
@@ -227,6 +263,10 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, Cfg<QT>::CTAS)
     __syncthreads();
     tc::fence_after();
     const uint32_t tmem = s_tmem;
+    // RB: the rebuilding launch before this one may still be running until here
+    // (q and the tail were written before that one began)
+    if (RB) asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     volatile int *abort_flag = &s_abort;
     auto wait = [&](uint64_t *bar, int parity, int code) {
         if (mbar_wait(bar, (uint32_t)parity, abort_flag)) return true;
@@ -238,16 +278,37 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, Cfg<QT>::CTAS)
     if (warp == 4 * QT) {
         // ------------------------------------------------------- TMA
         if (lane == 0) {
+            const RebuiltRows rb = RB ? rebuilt_rows(Tb, a.n_tail, a.n, a.window, a.sinks) : RebuiltRows{0, 0};
             int it = 0;
-            for (; it < 2 * nt; it++) {   // K and V tiles in turn
+            bool ok = true;
+            // a K or V tile into the next stage: rows from y on of (sequence, head) z, or of the tail
+            auto load = [&](const CUtensorMap *map, int y, bool tail) {
                 const int s = it % NS;
-                if (it >= NS && !wait(&bar_empty[s], (it / NS - 1) & 1, 31)) break;
-                const int tok = runs.token(j0 + (it >> 1));
-                const CUtensorMap *map = (it & 1) ? &map_v : &map_k;
+                if (ok && it >= NS) ok = wait(&bar_empty[s], (it / NS - 1) & 1, 31);
+                if (!ok) return;
                 const uint32_t dst = sstage + s * kStageBytes;
                 expect_tx(&bar_full[s], kStageBytes);
-                tma_3d(dst, map, 0, tok, b * a.H + h, &bar_full[s]);
-                tma_3d(dst + kBlkBytes, map, 64, tok, b * a.H + h, &bar_full[s]);
+                if (tail) {
+                    tma_4d(dst, map, 0, h, y, b, &bar_full[s]);
+                    tma_4d(dst + kBlkBytes, map, 64, h, y, b, &bar_full[s]);
+                } else {
+                    tma_3d(dst, map, 0, y, z, &bar_full[s]);
+                    tma_3d(dst + kBlkBytes, map, 64, y, z, &bar_full[s]);
+                }
+                it++;
+            };
+            for (int j = 0; j < nt && ok; j++) {
+                const int t = runs.token(j0 + j);
+                if (RB && j < nc) {
+                    const int y = j0 + j < runs.sink_tiles ? t : rb.sink_pad + t - rb.w_base;
+                    load(&maps.k, y, false);
+                    load(&maps.k_lo, y, false);
+                    load(&maps.v, y, false);
+                    if (SPLIT) load(&maps.v_lo, y, false);
+                } else {
+                    load(RB ? &maps.tail_k : &maps.k, t, RB);
+                    load(RB ? &maps.tail_v : &maps.v, t, RB);
+                }
             }
             // every issued load must have landed before the CTA exits
             for (int i = max(0, it - NS); i < it; i++) mbar_wait<256>(&bar_full[i % NS], (i / NS) & 1, abort_flag);
@@ -259,42 +320,54 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, Cfg<QT>::CTAS)
             constexpr uint32_t idS = tc::idesc_bf16(kTileR, kTileT, false);   // K: K-major
             constexpr uint32_t idO = tc::idesc_bf16(kTileR, kHeadDim, true);  // V: MN-major
             auto logits = [&](int q, int j) {
-                const int s = (2 * j) % NS;
-                const uint64_t da = tc::desc_k(sbase + q * kStageBytes), db = tc::desc_k(sstage + s * kStageBytes);
+                const uint64_t da = tc::desc_k(sbase + q * kStageBytes);
+                const int parts = RB && j < nc ? 2 : 1;
+                for (int p = 0; p < parts; p++) {
+                    const int s = (kstage(j) + p) % NS;
+                    const uint64_t db = tc::desc_k(sstage + s * kStageBytes);
 #pragma unroll
-                for (int kk = 0; kk < 8; kk++) {
-                    const uint64_t o = (uint64_t)(((kk >> 2) * kBlkBytes + (kk & 3) * 32) >> 4);
-                    tc::mma_bf16(tmem + q * 256, da + o, db + o, idS, kk > 0);
+                    for (int kk = 0; kk < 8; kk++) {
+                        const uint64_t o = (uint64_t)(((kk >> 2) * kBlkBytes + (kk & 3) * 32) >> 4);
+                        tc::mma_bf16(tmem + q * 256, da + o, db + o, idS, p > 0 || kk > 0);
+                    }
+                    if (q == QT - 1) tc::commit(&bar_empty[s]);
                 }
                 tc::commit(&bar_sfull[q]);
-                if (q == QT - 1) tc::commit(&bar_empty[s]);
             };
             auto values = [&](int q, int j) {
-                const int s = (2 * j + 1) % NS;
-                const uint64_t dv = tc::desc_mn(sstage + s * kStageBytes, kBlkBytes);
-#pragma unroll
-                for (int part = 0; part < (SPLIT ? 2 : 1); part++)
+                // (P part, V part): hi hi, lo hi, hi lo
+                const int terms = !SPLIT ? 1 : RB && j < nc ? 3 : 2;
+                for (int p = 0; p < terms; p++) {
+                    const int s = (vstage(j) + (p == 2 ? 1 : 0)) % NS;
+                    const uint64_t dv = tc::desc_mn(sstage + s * kStageBytes, kBlkBytes);
+                    const uint32_t pa = tmem + q * 256 + (p == 1 ? 64 : 0);
 #pragma unroll
                     for (int kk = 0; kk < 8; kk++)
-                        mma_ts(tmem + q * 256 + 128, tmem + q * 256 + part * 64 + kk * 8, dv + (uint64_t)((kk * 2048) >> 4),
-                               idO, j > 0 || part > 0 || kk > 0);
-                if (q == QT - 1) tc::commit(&bar_empty[s]);
+                        mma_ts(tmem + q * 256 + 128, pa + kk * 8, dv + (uint64_t)((kk * 2048) >> 4), idO,
+                               j > 0 || p > 0 || kk > 0);
+                    if (q == QT - 1 && (p == 2 || p == min(terms, 2) - 1)) tc::commit(&bar_empty[s]);
+                }
                 if (j == nt - 1) tc::commit(&bar_ofull[q]);
             };
-            bool ok = nt == 0 || wait(&bar_full[0], 0, 32);
+            auto loaded = [&](int i, int code) { return wait(&bar_full[i % NS], (i / NS) & 1, code); };
+            auto k_loaded = [&](int j) { return loaded(kstage(j), 32) && (!(RB && j < nc) || loaded(kstage(j) + 1, 33)); };
+            auto v_loaded = [&](int j) {
+                return loaded(vstage(j), 34) && (!(RB && SPLIT && j < nc) || loaded(vstage(j) + 1, 35));
+            };
+            bool ok = nt == 0 || k_loaded(0);
             if (nt > 0 && ok) {
                 tc::fence_after();
                 for (int q = 0; q < QT; q++) logits(q, 0);
             }
             for (int j = 0; j < nt && ok; j++) {
-                ok = wait(&bar_full[(2 * j + 1) % NS], ((2 * j + 1) / NS) & 1, 33);
+                ok = v_loaded(j);
                 for (int q = 0; q < QT && ok; q++) {
-                    ok = wait(&bar_pfull[q], j & 1, 34);
+                    ok = wait(&bar_pfull[q], j & 1, 36);
                     if (!ok) break;
                     tc::fence_after();
                     values(q, j);
                     if (j + 1 < nt) {
-                        if (q == 0) ok = wait(&bar_full[(2 * j + 2) % NS], ((2 * j + 2) / NS) & 1, 35);
+                        if (q == 0) ok = k_loaded(j + 1);
                         if (!ok) break;
                         logits(q, j + 1);
                     }
@@ -307,22 +380,30 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, Cfg<QT>::CTAS)
         const int q = warp >> 2;                       // row tile
         const int row = q * kTileR + (warp & 3) * 32 + lane;
         const bool live = q * kTileR + (warp & 3) * 32 < nr;   // warp-uniform: some row of the warp exists
-        const int pos = Tb - a.n + (r0 + row) / a.G;   // the row's position
+        const int pos = Tb + a.n_tail - a.n + (r0 + row) / a.G;   // the row's position
         const int lim = pos + 1;
         const int lo = (int)max(0ll, (long long)pos + 1 - a.window);
         const uint32_t tS = tmem + q * 256 + ((uint32_t)(32 * (warp & 3)) << 16), tO = tS + 128;
         const bool careful = __ldcg(a.nonfinite) != 0;
         float m_used = -CUDART_INF_F, l = 0.f;
         for (int j = 0; j < nt; j++) {
-            const int tb = runs.token(j0 + j);
-            // a sinks' tile may reach into the window's: its part ends where that begins
-            const int end = j0 + j < runs.sink_tiles ? min(lim, runs.w_tile) : lim;
+            // positions tb .. of the tile's tokens; a sinks' tile may reach into the
+            // window's, a committed one (RB) past the sequence's committed tokens
+            const bool in_tail = j0 + j >= runs.committed;
+            const int tb = runs.token(j0 + j) + (in_tail ? Tb : 0);
+            const int end = j0 + j < runs.sink_tiles ? min(lim, runs.sink_end) : in_tail ? lim : min(lim, Tb);
+            wait(&bar_sfull[q], j & 1, 38);
+            tc::fence_after();
             if (careful) {
-                // V rows that are not finite become zeros with a flag (thread t: token t)
+                // V rows that are not finite become zeros with a flag (thread t: token t);
+                // after S, so that the stage's phase before V's is known to be over
                 asm volatile("bar.sync 1, %0;" ::"n"(128 * QT) : "memory");
                 if (q == 0) {
-                    const int s = (2 * j + 1) % NS, t = tid;
-                    wait(&bar_full[s], ((2 * j + 1) / NS) & 1, 36);
+                    const int s = vstage(j) % NS, t = tid;
+                    wait(&bar_full[s], (vstage(j) / NS) & 1, 37);
+                    const int s_lo = (vstage(j) + 1) % NS;
+                    const bool has_lo = RB && SPLIT && j < nc;
+                    if (has_lo) wait(&bar_full[s_lo], ((vstage(j) + 1) / NS) & 1, 37);
                     uint32_t bad = 0;
                     for (int c = 0; c < 16; c++) {
                         const uint4 v = *reinterpret_cast<const uint4 *>(stages + s * kStageBytes + (c >> 3) * kBlkBytes +
@@ -332,16 +413,14 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, Cfg<QT>::CTAS)
                         for (int i = 0; i < 4; i++) bad |= ((w[i] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
                     }
                     if (bad)
-                        for (int c = 0; c < 16; c++)
-                            *reinterpret_cast<uint4 *>(stages + s * kStageBytes + (c >> 3) * kBlkBytes + t * 128 +
-                                                       (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        for (int c = 0; c < (has_lo ? 32 : 16); c++)
+                            *reinterpret_cast<uint4 *>(stages + (c < 16 ? s : s_lo) * kStageBytes + ((c >> 3) & 1) * kBlkBytes +
+                                                       t * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
                     s_bad[t] = bad ? 1 : 0;
                     tc::fence_async_smem();
                 }
                 asm volatile("bar.sync 1, %0;" ::"n"(128 * QT) : "memory");
             }
-            wait(&bar_sfull[q], j & 1, 37);
-            tc::fence_after();
             if (live) {
                 uint32_t s[128];
 #pragma unroll
@@ -424,7 +503,7 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, Cfg<QT>::CTAS)
         }
         // ------------------------------------------------------- output
         if (nt > 0) {
-            wait(&bar_ofull[q], 0, 38);
+            wait(&bar_ofull[q], 0, 39);
             tc::fence_after();
         }
         if (live) {
@@ -479,46 +558,48 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, Cfg<QT>::CTAS)
         tc::fence_after();
         tc::dealloc(tmem, C::COLS);
     }
-    // ----------------------------------------------------------- split merge
-    // The last split of the row block to arrive merges every split's partial
-    // of its rows; it leaves the counter at zero for the next launch.
-    if (a.S > 1) {
-        __threadfence();
-        __syncthreads();
-        const int unit = (b * a.H + h) * a.nqb + qb;
-        if (tid == 0) s_last = atomicAdd(a.counters + unit, 1) == a.S - 1;
-        __syncthreads();
-        if (!s_last) return;
-        __threadfence();
-        for (int row = warp; row < nr; row += C::THREADS / 32) {
-            const int rg = r0 + row, t = rg / a.G, gq = rg % a.G;
-            const size_t prow = ((size_t)b * a.n + t) * a.Hq + h * a.G + gq;
-            const float *part = a.partials + prow * a.S * kPartialStride;
-            float M = -CUDART_INF_F, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int sp = 0; sp < a.S; sp++) {
-                const float *p = part + (size_t)sp * kPartialStride;
-                const float m = __ldcg(p + kHeadDim), ls = __ldcg(p + kHeadDim + 1);
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(p) + lane);
-                if (m == -CUDART_INF_F && ls == 0.f) continue;   // uniform over the warp: no key in this split
-                const float Mn = fmaxf(M, m);
-                const float c0 = M == -CUDART_INF_F ? 0.f : exp2f(M - Mn), c = m == -CUDART_INF_F ? 1.f : exp2f(m - Mn);
-                l = fmaf(ls, c, l * c0);
-                o[0] = fmaf(v.x, c, o[0] * c0);
-                o[1] = fmaf(v.y, c, o[1] * c0);
-                o[2] = fmaf(v.z, c, o[2] * c0);
-                o[3] = fmaf(v.w, c, o[3] * c0);
-                M = Mn;
-            }
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            if (a.out16)
-                *reinterpret_cast<uint2 *>(a.out16 + prow * kHeadDim + 4 * lane) =
-                    make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
-            else
-                *reinterpret_cast<float4 *>(a.out + prow * kHeadDim + 4 * lane) =
-                    make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+}
+
+// Merges the split partials of the output rows: a warp per row.  A launch of its
+// own -- the last CTA of a row block merging its 128 rows, as the other kernels
+// do for few rows, took up to 40 us.
+__global__ void __launch_bounds__(128) merge_rows_kernel(const Bf16Args a, long long rows) {
+    const int lane = threadIdx.x & 31;
+    const long long prow = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (prow >= rows) return;   // uniform per warp
+    const float *part = a.partials + (size_t)prow * a.S * kPartialStride;
+    float M = -CUDART_INF_F, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int s0 = 0; s0 < a.S; s0 += kMerge) {   // a batch's loads are in flight together
+        float m[kMerge], ls[kMerge];
+        float4 v[kMerge];
+#pragma unroll
+        for (int u = 0; u < kMerge; u++) {
+            const float *p = part + (size_t)min(s0 + u, a.S - 1) * kPartialStride;
+            m[u] = __ldcg(p + kHeadDim);
+            ls[u] = __ldcg(p + kHeadDim + 1);
+            v[u] = __ldcg(reinterpret_cast<const float4 *>(p) + lane);
         }
-        if (tid == 0) a.counters[unit] = 0;
+#pragma unroll
+        for (int u = 0; u < kMerge; u++) {
+            if (s0 + u >= a.S || (m[u] == -CUDART_INF_F && ls[u] == 0.f)) continue;   // uniform: no key in this split
+            const float Mn = fmaxf(M, m[u]);
+            const float c0 = M == -CUDART_INF_F ? 0.f : exp2f(M - Mn), c = m[u] == -CUDART_INF_F ? 1.f : exp2f(m[u] - Mn);
+            l = fmaf(ls[u], c, l * c0);
+            o[0] = fmaf(v[u].x, c, o[0] * c0);
+            o[1] = fmaf(v[u].y, c, o[1] * c0);
+            o[2] = fmaf(v[u].z, c, o[2] * c0);
+            o[3] = fmaf(v[u].w, c, o[3] * c0);
+            M = Mn;
+        }
     }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (a.out16)
+        *reinterpret_cast<uint2 *>(a.out16 + prow * kHeadDim + 4 * lane) =
+            make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
+    else
+        *reinterpret_cast<float4 *>(a.out + prow * kHeadDim + 4 * lane) =
+            make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
 }
 
 // cuTensorMapEncodeTiled through the runtime (the library links no libcuda).
@@ -539,28 +620,63 @@ EncodeFn encode_fn() {
     return fn;
 }
 
-// K or V of a BF16 cache, [B * H][Tp][128]: boxes of 128 tokens x 64 elements,
-// 128-byte swizzled; rows past Tp read as zeros.
-bool make_map(CUtensorMap *map, const uint16_t *base, int Tp, long long heads) {
+bool encode(CUtensorMap *map, const uint16_t *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
+            const cuuint32_t *box) {
     const EncodeFn fn = encode_fn();
-    if (!fn) return false;
-    const cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)Tp, (cuuint64_t)heads};
-    const cuuint64_t strides[2] = {kHeadDim * 2, (cuuint64_t)Tp * kHeadDim * 2};
-    const cuuint32_t box[3] = {64, kTileT, 1}, step[3] = {1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t *>(base), dims, strides, box, step,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint32_t step[4] = {1, 1, 1, 1};
+    return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<uint16_t *>(base), dims, strides, box, step,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// [heads][rows][128] BF16 (a BF16 cache's K or V with rows = Tp, or the rebuilt
+// rows): boxes of 128 rows x 64 elements, 128-byte swizzled; rows past the last
+// read as zeros.
+bool make_map(CUtensorMap *map, const uint16_t *base, long long rows, long long heads) {
+    const cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)rows, (cuuint64_t)heads};
+    const cuuint64_t strides[2] = {kHeadDim * 2, (cuuint64_t)rows * kHeadDim * 2};
+    const cuuint32_t box[3] = {64, kTileT, 1};
+    return encode(map, base, 3, dims, strides, box);
+}
+// The tail [B][cap][H][128]: the same boxes of one head.
+bool make_tail_map(CUtensorMap *map, const uint16_t *base, int B, int cap, int H) {
+    const cuuint64_t dims[4] = {(cuuint64_t)kHeadDim, (cuuint64_t)H, (cuuint64_t)cap, (cuuint64_t)B};
+    const cuuint64_t strides[3] = {kHeadDim * 2, (cuuint64_t)H * kHeadDim * 2, (cuuint64_t)cap * H * kHeadDim * 2};
+    const cuuint32_t box[4] = {64, 1, kTileT, 1};
+    return encode(map, base, 4, dims, strides, box);
 }
 
-template <int QT, bool SPLIT>
-cudaError_t launch_t(const CUtensorMap &mk, const CUtensorMap &mv, const Bf16Args &a, cudaStream_t st) {
+// A launch that may begin while the one before it on the stream still runs.
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*f)(P...), dim3 grid, int threads, int smem, bool overlap, cudaStream_t st, A... args) {
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = grid;
+    lc.blockDim = dim3(threads);
+    lc.dynamicSmemBytes = smem;
+    lc.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = overlap ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&lc, f, args...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int QT, bool SPLIT, bool RB>
+cudaError_t launch_t(const Maps &m, const Bf16Args &a, cudaStream_t st) {
     static bool done[kMaxDevices];
     cudaError_t e = once_per_device(done, [] {
-        return cudaFuncSetAttribute(prefill_bf16_kernel<QT, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<QT>::SMEM);
+        return cudaFuncSetAttribute(prefill_bf16_kernel<QT, SPLIT, RB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    Cfg<QT>::SMEM);
     });
     if (e != cudaSuccess) return e;
-    prefill_bf16_kernel<QT, SPLIT><<<dim3(a.S, a.H, a.B * a.nqb), Cfg<QT>::THREADS, Cfg<QT>::SMEM, st>>>(mk, mv, a);
-    return cudaGetLastError();
+    return launch_overlapped(prefill_bf16_kernel<QT, SPLIT, RB>, dim3(a.S, a.heads, a.B * a.nqb), Cfg<QT>::THREADS,
+                             Cfg<QT>::SMEM, RB, st, m, a);
+}
+template <bool RB>
+cudaError_t launch_rb(int qt, const Maps &m, const Bf16Args &a, cudaStream_t st) {
+    if (qt == 1) return a.out16 ? launch_t<1, false, RB>(m, a, st) : launch_t<1, true, RB>(m, a, st);
+    return a.out16 ? launch_t<2, false, RB>(m, a, st) : launch_t<2, true, RB>(m, a, st);
 }
 
 // Row tiles per CTA: two share their K and V tiles; one while there are no
@@ -581,7 +697,7 @@ void prefill_bf16_plan(PrefillArgs *a, int sms) {
     int nt = 1;
     for (int b = 0; b < a->B; b++)
         for (int r0 = 0; r0 < nq; r0 += rows) {
-            const int t = Runs(a->seqT.v[b], a->n, r0 / a->G, (std::min(r0 + rows, nq) - 1) / a->G, a->window, a->sinks).tiles;
+            const int t = Runs(a->seqT.v[b], a->n_tail, a->n, r0 / a->G, (std::min(r0 + rows, nq) - 1) / a->G, a->window, a->sinks).tiles;
             total += t;
             nt = std::max(nt, t);
         }
@@ -602,17 +718,12 @@ void prefill_bf16_plan(PrefillArgs *a, int sms) {
     }
 }
 
-cudaError_t launch_prefill_bf16(const PrefillArgs &p, const uint16_t *k, const uint16_t *v, const int *nonfinite, int sms,
-                                cudaStream_t st) {
-    CUtensorMap mk, mv;
-    const long long heads = (long long)p.B * p.H;
-    if (!make_map(&mk, k, p.Tp, heads) || !make_map(&mv, v, p.Tp, heads)) return cudaErrorInvalidValue;
+static Bf16Args bf16_args(const PrefillArgs &p, const int *nonfinite) {
     Bf16Args a;
     a.q = p.q;
     a.partials = p.partials;
     a.out = p.out;
     a.out16 = p.out16;
-    a.counters = p.counters;
     a.err = p.err;
     a.nonfinite = nonfinite;
     a.seqT = p.seqT;
@@ -621,13 +732,48 @@ cudaError_t launch_prefill_bf16(const PrefillArgs &p, const uint16_t *k, const u
     a.Hq = p.Hq;
     a.G = p.G;
     a.n = p.n;
+    a.n_tail = p.n_tail;
     a.S = p.S;
     a.nqb = p.nqb;
     a.window = p.window;
     a.sinks = p.sinks;
     a.scale_log2 = p.scale_log2;
-    if (row_tiles(p, sms) == 1) return p.out16 ? launch_t<1, false>(mk, mv, a, st) : launch_t<1, true>(mk, mv, a, st);
-    return p.out16 ? launch_t<2, false>(mk, mv, a, st) : launch_t<2, true>(mk, mv, a, st);
+    a.h0 = 0;
+    a.heads = p.H;
+    return a;
+}
+
+cudaError_t launch_prefill_bf16(const PrefillArgs &p, const uint16_t *k, const uint16_t *v, const int *nonfinite, int sms,
+                                cudaStream_t st) {
+    Maps m;
+    std::memset(&m, 0, sizeof(m));
+    const long long heads = (long long)p.B * p.H;
+    if (!make_map(&m.k, k, p.Tp, heads) || !make_map(&m.v, v, p.Tp, heads)) return cudaErrorInvalidValue;
+    return launch_rb<false>(row_tiles(p, sms), m, bf16_args(p, nonfinite), st);
+}
+
+cudaError_t launch_prefill_rebuilt(const PrefillArgs &p, const ReadArgs &r, int sms, cudaStream_t st) {
+    Maps m;
+    std::memset(&m, 0, sizeof(m));
+    const long long heads = (long long)p.B * r.H;
+    const bool lo = !p.out16;
+    if (!make_map(&m.k, static_cast<const uint16_t *>(r.out[0]), r.pair_stride, heads) ||
+        !make_map(&m.k_lo, r.out_lo[0], r.pair_stride, heads) ||
+        !make_map(&m.v, static_cast<const uint16_t *>(r.out[1]), r.pair_stride, heads) ||
+        (lo && !make_map(&m.v_lo, r.out_lo[1], r.pair_stride, heads)) ||
+        (p.n_tail > 0 && (!make_tail_map(&m.tail_k, p.tail_k, p.B, p.tail_cap, p.H) ||
+                          !make_tail_map(&m.tail_v, p.tail_v, p.B, p.tail_cap, p.H))))
+        return cudaErrorInvalidValue;
+    Bf16Args a = bf16_args(p, r.nonfinite);
+    a.h0 = r.h0;
+    a.heads = r.H;
+    return launch_rb<true>(row_tiles(p, sms), m, a, st);
+}
+
+cudaError_t launch_merge_rows(const PrefillArgs &p, cudaStream_t st) {
+    const long long rows = (long long)p.B * p.n * p.Hq;
+    if ((rows + 3) / 4 > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+    return launch_overlapped(merge_rows_kernel, dim3((unsigned)((rows + 3) / 4)), 128, 0, true, st, bf16_args(p, nullptr), rows);
 }
 
 }  // namespace rq

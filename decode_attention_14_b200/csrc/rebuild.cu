@@ -1,0 +1,35 @@
+// rebuild.cu -- the rows that a chunk of new tokens attends to, rebuilt from the
+// compressed cache as BF16 pairs in a workspace (first half of
+// rq_prefill_attn_window on chunks of many rows): the kOutPair instantiations
+// of read.cuh.
+#include "read.cuh"
+
+namespace rq {
+namespace {
+
+template <int BA, int BR, int GS>
+cudaError_t launch_group(const ReadArgs &a, unsigned blocks, cudaStream_t st) {
+    if (a.nr == 0) return launch_t<BA, 2, GS, 0, false, kOutPair>(a, blocks, st);
+    return a.rotate ? launch_t<BA, BR, GS, 1, true, kOutPair>(a, blocks, st)
+                    : launch_t<BA, BR, GS, 1, false, kOutPair>(a, blocks, st);
+}
+template <int BA, int BR>
+cudaError_t launch_bits(const ReadArgs &a, unsigned blocks, cudaStream_t st) {
+    return a.g == 16 ? launch_group<BA, BR, 16>(a, blocks, st) : launch_group<BA, BR, 32>(a, blocks, st);
+}
+
+}  // namespace
+
+cudaError_t launch_rebuild(const ReadArgs &args, int ba, int br, cudaStream_t st) {
+    ReadArgs a = args;
+    const long long units = 2LL * a.B * a.H, nt = a.pair_rows / kRecs;
+    a.tiles = warp_tiles(units * nt);
+    const int per = a.tiles * kWarps;
+    const long long blocks = units * ((nt + per - 1) / per);
+    if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+    const unsigned nb = (unsigned)blocks;
+    if (ba == 4) return br == 2 ? launch_bits<4, 2>(a, nb, st) : launch_bits<4, 4>(a, nb, st);
+    return launch_bits<2, 2>(a, nb, st);
+}
+
+}  // namespace rq

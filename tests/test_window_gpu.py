@@ -13,7 +13,9 @@ output moves by at most twice that times the values' spread: 2e-4 max abs and
 2e-5 relative L2 leave a margin for fp32 sums.  The chunk kernel splits
 probabilities and rotated queries into BF16 pairs (relative 2^-17 each): the
 contract's 1e-3 / 2e-3.  BF16 caches: fp32 products and sums (decode), or
-probabilities as BF16 pairs.  BF16 output adds half a step, 2^-8 |x|.
+probabilities as BF16 pairs.  BF16 output adds half a step, 2^-8 |x|; a chunk's
+weights and (compressed cache) values are then BF16 too, 2^-9 of each: at most
+2 * 2^-9 max|v| with |v| < 45, and 2^-8 of the row's norm at random signs.
 """
 import numpy as np
 import pytest
@@ -284,7 +286,9 @@ def test_window_refusals():
 
 
 # ------------------------------------------------------------------ several tokens
-def chunk_check(bt, loop, lens, n, window, sinks, dtype=torch.float32, seed=11, rel=1e-3, mx=2e-3):
+def chunk_check(bt, loop, lens, n, window, sinks, dtype=torch.float32, seed=11, rel=None, mx=None):
+    rel = rel or (1e-3 if dtype == torch.float32 else 2.0 ** -8)
+    mx = mx or (2e-3 if dtype == torch.float32 else 0.18)
     q = queries(seed, bt.cfg.batch, n, bt.cfg.num_q_heads, 128)
     ref = reference(keys_values(bt, 0, loop, lens), q, window, sinks)
     check(bt.cache.prefill_window(0, loop, q, window, sinks, dtype=dtype), ref, rel, mx)
@@ -554,3 +558,24 @@ def test_bf16_prefill_repeats_itself():
     assert e.value.status == rq.RQ_ERR_STATE
     bt.cache.check()
     bt.cache.close()
+
+
+def test_prefill_window_beyond_one_workspace():
+    """More rebuilt rows than the workspace holds at once (4 GiB): the kv heads go in groups.  8 sequences of 160 000
+    tokens at an anchor loop; the last token's row against the single-token call, for every head."""
+    B, Hk, T = 8, 4, 160000
+    cfg = rq.make_config(num_layers=1, num_loops=1, loops_per_group=1, batch=B, max_tokens=T, max_tail_tokens=0,
+                         num_kv_heads=Hk, num_q_heads=Hk)
+    cache = H.guarded_cache(cfg)
+    g = torch.Generator("cuda").manual_seed(3)
+    for t in range(0, T, 20000):
+        k, v = (torch.randn((B, 20000, Hk, 128), generator=g, device="cuda").bfloat16() for _ in range(2))
+        cache.append(0, 0, k, v)
+    q = queries(17, B, 3, Hk, 128)
+    got = cache.prefill_window(0, 0, q, 0)
+    ref = cache.decode_window(0, 0, q[:, -1].contiguous(), 0).double().cpu().numpy()
+    for h in range(Hk):
+        g_h, r_h = got[:, -1, h].double().cpu().numpy(), ref[:, h]
+        assert np.linalg.norm(g_h - r_h) <= 1e-3 * np.linalg.norm(r_h) and np.abs(g_h - r_h).max() <= 2e-3, h
+    cache.check()
+    cache.close()
