@@ -16,10 +16,12 @@
 //               P as a BF16 high and low part, relative 2^-17, for fp32 output;
 //               for BF16 output P is rounded to BF16, half a step of which,
 //               2^-9 of each weight, is as small as the output's own rounding)
-// P overwrites S in tensor memory: S (128 columns) and O (128) per row tile.
-// With QT = 2 one row tile's MMAs run while the other's softmax does, and both
+// P overwrites S in tensor memory; O is beside it (128 columns each).  Two S
+// buffers keep the tensor cores and the softmax busy at once: with QT = 2 one
+// per row tile -- one tile's MMAs run while the other's softmax does, and both
 // share every K and V tile, which halves the L2 traffic (a 128 x 128 tile pair
-// is 64 KB for 2 x 1024 tensor cycles); with QT = 1 two CTAs share an SM.
+// is 64 KB for 2 x 1024 tensor cycles); with QT = 1 (few rows) one per parity
+// of the token tile.
 // Several splits' partials are merged by a launch of its own.
 //
 // Warps: 4 QT softmax warps (a thread per row: tensor-memory lane = row), then
@@ -28,10 +30,11 @@
 // Hand-offs, all bounded waits (error word, abort flag):
 //   full[s]   TMA -> MMA          stage s loaded
 //   empty[s]  MMA commit -> TMA   stage s read
-//   sfull[q]  MMA commit -> softmax   S of row tile q complete, and with it all
-//             MMAs issued before, the values of the tile before among them
-//   pfull[q]  softmax -> MMA      P of row tile q written
-//   ofull[q]  MMA commit -> softmax   the last values complete
+//   sfull[i]  MMA commit -> softmax   S buffer i complete, and with it all MMAs
+//             issued before (QT = 2: the values of the tile before among them)
+//   pfull[i]  softmax -> MMA      P written over S buffer i
+//   odone[q]  MMA commit -> softmax   values of a tile complete (before O is
+//             rescaled with QT = 1, and at the end)
 //
 // RB: the same over a compressed cache.  A first launch (rebuild.cu) writes the
 // committed tokens that the chunk sees as BF16 high and low parts into a
@@ -72,11 +75,10 @@ constexpr int kMerge = 8;                            // split partials of a row 
 
 template <int QT>
 struct Cfg {
-    static constexpr int STAGES = QT == 2 ? 5 : 2;
+    static constexpr int STAGES = 7 - QT;
     static constexpr int THREADS = 32 * (4 * QT + 2);
-    static constexpr int CTAS = QT == 2 ? 1 : 2;
     static constexpr int SMEM = (QT + STAGES) * kStageBytes + 1024;   // + alignment of the base
-    static constexpr uint32_t COLS = 256 * QT;       // S and O of each row tile
+    static constexpr uint32_t COLS = 512;            // S buffers at columns 0 and 128, O of row tile q at 256 + 128 q
 };
 
 // ---------------------------------------------------------------- PTX helpers
@@ -197,12 +199,12 @@ struct Runs {
 };
 
 template <int QT, bool SPLIT, bool RB>
-__global__ void __launch_bounds__(Cfg<QT>::THREADS, Cfg<QT>::CTAS)
+__global__ void __launch_bounds__(Cfg<QT>::THREADS, 1)
     prefill_bf16_kernel(const __grid_constant__ Maps maps, const Bf16Args a) {
     using C = Cfg<QT>;
     constexpr int NS = C::STAGES;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t bar_full[NS], bar_empty[NS], bar_sfull[QT], bar_pfull[QT], bar_ofull[QT];
+    __shared__ uint64_t bar_full[NS], bar_empty[NS], bar_sfull[2], bar_pfull[2], bar_odone[QT];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     __shared__ uint8_t s_bad[kTileT];
@@ -227,6 +229,9 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, Cfg<QT>::CTAS)
     // low, V (SPLIT: high and low); kstage / vstage are its first of each.
     constexpr int CST = SPLIT ? 4 : 3;
     const int nc = RB ? max(0, min(j1, runs.committed) - j0) : 0;   // rebuilt tiles
+    // S buffer of row tile q's token tile j, and the parity of its phase then
+    auto sbuf = [](int q, int j) { return QT == 2 ? q : j & 1; };
+    auto sphase = [](int j) { return QT == 2 ? j & 1 : (j >> 1) & 1; };
     auto kstage = [&](int j) { return RB ? (j <= nc ? CST * j : CST * nc + 2 * (j - nc)) : 2 * j; };
     auto vstage = [&](int j) { return kstage(j) + (RB && j < nc ? 2 : 1); };
 
@@ -235,11 +240,11 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, Cfg<QT>::CTAS)
             mbar_init(&bar_full[i], 1);
             mbar_init(&bar_empty[i], 1);
         }
-        for (int i = 0; i < QT; i++) {
+        for (int i = 0; i < 2; i++) {
             mbar_init(&bar_sfull[i], 1);
             mbar_init(&bar_pfull[i], 4);   // a lane of each of its softmax warps
-            mbar_init(&bar_ofull[i], 1);
         }
+        for (int i = 0; i < QT; i++) mbar_init(&bar_odone[i], 1);
         s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -328,11 +333,11 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, Cfg<QT>::CTAS)
 #pragma unroll
                     for (int kk = 0; kk < 8; kk++) {
                         const uint64_t o = (uint64_t)(((kk >> 2) * kBlkBytes + (kk & 3) * 32) >> 4);
-                        tc::mma_bf16(tmem + q * 256, da + o, db + o, idS, p > 0 || kk > 0);
+                        tc::mma_bf16(tmem + sbuf(q, j) * 128, da + o, db + o, idS, p > 0 || kk > 0);
                     }
                     if (q == QT - 1) tc::commit(&bar_empty[s]);
                 }
-                tc::commit(&bar_sfull[q]);
+                tc::commit(&bar_sfull[sbuf(q, j)]);
             };
             auto values = [&](int q, int j) {
                 // (P part, V part): hi hi, lo hi, hi lo
@@ -340,36 +345,40 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, Cfg<QT>::CTAS)
                 for (int p = 0; p < terms; p++) {
                     const int s = (vstage(j) + (p == 2 ? 1 : 0)) % NS;
                     const uint64_t dv = tc::desc_mn(sstage + s * kStageBytes, kBlkBytes);
-                    const uint32_t pa = tmem + q * 256 + (p == 1 ? 64 : 0);
+                    const uint32_t pa = tmem + sbuf(q, j) * 128 + (p == 1 ? 64 : 0);
 #pragma unroll
                     for (int kk = 0; kk < 8; kk++)
-                        mma_ts(tmem + q * 256 + 128, pa + kk * 8, dv + (uint64_t)((kk * 2048) >> 4), idO,
+                        mma_ts(tmem + 256 + q * 128, pa + kk * 8, dv + (uint64_t)((kk * 2048) >> 4), idO,
                                j > 0 || p > 0 || kk > 0);
                     if (q == QT - 1 && (p == 2 || p == min(terms, 2) - 1)) tc::commit(&bar_empty[s]);
                 }
-                if (j == nt - 1) tc::commit(&bar_ofull[q]);
+                tc::commit(&bar_odone[q]);
             };
             auto loaded = [&](int i, int code) { return wait(&bar_full[i % NS], (i / NS) & 1, code); };
             auto k_loaded = [&](int j) { return loaded(kstage(j), 32) && (!(RB && j < nc) || loaded(kstage(j) + 1, 33)); };
             auto v_loaded = [&](int j) {
                 return loaded(vstage(j), 34) && (!(RB && SPLIT && j < nc) || loaded(vstage(j) + 1, 35));
             };
-            bool ok = nt == 0 || k_loaded(0);
-            if (nt > 0 && ok) {
+            // logits run AHEAD tiles before values: with QT = 1 into the other S buffer
+            constexpr int AHEAD = QT == 2 ? 1 : 2;
+            bool ok = true;
+            for (int j = 0; j < min(AHEAD, nt) && ok; j++) {
+                ok = k_loaded(j);
+                if (!ok) break;
                 tc::fence_after();
-                for (int q = 0; q < QT; q++) logits(q, 0);
+                for (int q = 0; q < QT; q++) logits(q, j);
             }
             for (int j = 0; j < nt && ok; j++) {
                 ok = v_loaded(j);
                 for (int q = 0; q < QT && ok; q++) {
-                    ok = wait(&bar_pfull[q], j & 1, 36);
+                    ok = wait(&bar_pfull[sbuf(q, j)], sphase(j), 36);
                     if (!ok) break;
                     tc::fence_after();
                     values(q, j);
-                    if (j + 1 < nt) {
-                        if (q == 0) ok = k_loaded(j + 1);
+                    if (j + AHEAD < nt) {
+                        if (q == 0) ok = k_loaded(j + AHEAD);
                         if (!ok) break;
-                        logits(q, j + 1);
+                        logits(q, j + AHEAD);
                     }
                 }
             }
@@ -383,7 +392,7 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, Cfg<QT>::CTAS)
         const int pos = Tb + a.n_tail - a.n + (r0 + row) / a.G;   // the row's position
         const int lim = pos + 1;
         const int lo = (int)max(0ll, (long long)pos + 1 - a.window);
-        const uint32_t tS = tmem + q * 256 + ((uint32_t)(32 * (warp & 3)) << 16), tO = tS + 128;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16), tO = lanes + 256 + q * 128;
         const bool careful = __ldcg(a.nonfinite) != 0;
         float m_used = -CUDART_INF_F, l = 0.f;
         for (int j = 0; j < nt; j++) {
@@ -392,7 +401,8 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, Cfg<QT>::CTAS)
             const bool in_tail = j0 + j >= runs.committed;
             const int tb = runs.token(j0 + j) + (in_tail ? Tb : 0);
             const int end = j0 + j < runs.sink_tiles ? min(lim, runs.sink_end) : in_tail ? lim : min(lim, Tb);
-            wait(&bar_sfull[q], j & 1, 38);
+            const uint32_t tS = lanes + sbuf(q, j) * 128;
+            wait(&bar_sfull[sbuf(q, j)], sphase(j), 38);
             tc::fence_after();
             if (careful) {
                 // V rows that are not finite become zeros with a flag (thread t: token t);
@@ -457,6 +467,12 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, Cfg<QT>::CTAS)
                 const float f = rescale ? exp2f(m_used - mx) : 1.f;
                 if (raise) m_used = mx;
                 if (__any_sync(0xffffffffu, rescale)) {
+                    // QT = 1: the values of tile j - 1 may still be running (those of j - 2 are
+                    // not: S of this tile came after them)
+                    if (QT == 1 && j > 0) {
+                        wait(&bar_odone[q], (j - 1) & 1, 40);
+                        tc::fence_after();
+                    }
 #pragma unroll 1
                     for (int c = 0; c < 4; c++) {
                         uint32_t v[32];
@@ -499,11 +515,14 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, Cfg<QT>::CTAS)
             }
             tc::fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar_pfull[q]);
+            if (lane == 0) mbar_arrive(&bar_pfull[sbuf(q, j)]);
         }
         // ------------------------------------------------------- output
         if (nt > 0) {
-            wait(&bar_ofull[q], 0, 39);
+            // (QT = 1: the last S says that the values of tile nt - 3 are complete, so the phase
+            // before the last is waited for first)
+            if (QT == 1 && nt > 1) wait(&bar_odone[q], nt & 1, 39);
+            wait(&bar_odone[q], (nt - 1) & 1, 39);
             tc::fence_after();
         }
         if (live) {
@@ -689,7 +708,7 @@ int row_tiles(const PrefillArgs &a, int sms) {
 }  // namespace
 
 void prefill_bf16_plan(PrefillArgs *a, int sms) {
-    const int rows = kTileR * row_tiles(*a, sms), slots = sms * (rows == kTileR ? Cfg<1>::CTAS : Cfg<2>::CTAS);
+    const int rows = kTileR * row_tiles(*a, sms), slots = sms;
     const int nq = a->n * a->G;
     a->nqb = (nq + rows - 1) / rows;
     // tiles of all row blocks, and of the longest
