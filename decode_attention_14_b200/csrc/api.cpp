@@ -1090,14 +1090,14 @@ int prefill_common(rq_cache *c, int layer, int loop, const void *q, int n, void 
     a.partials = c->prefill_ws;
     if (bf16) {
         s = cuda_status(launch_prefill_bf16(a, bf16_ptr(c, layer, loop, 0), bf16_ptr(c, layer, loop, 1), nonfinite_ptr(c),
-                                            c->sms, st));
+                                            st));
     } else {
         s = plan_rebuild(c, a, st, &rd);
         const int heads = rd.H;
         for (rd.h0 = 0; s == RQ_OK && rd.h0 < a.H; rd.h0 += heads) {
             rd.H = std::min(heads, a.H - rd.h0);
             s = cuda_status(launch_rebuild(rd, cfg.anchor_bits, cfg.resid_bits, st));
-            if (s == RQ_OK) s = cuda_status(launch_prefill_rebuilt(a, rd, c->sms, st));
+            if (s == RQ_OK) s = cuda_status(launch_prefill_rebuilt(a, rd, st));
         }
     }
     if (s == RQ_OK && a.S > 1) s = cuda_status(launch_merge_rows(a, st));

@@ -35,6 +35,7 @@ struct PrefillArgs {
     int tail_in_kernel;                // the attention kernel (last split) takes the tail tokens
     int window, sinks;                 // windowed calls: the query at position p sees (p - window, p] and [0, sinks)
     uint16_t *out16;                   // the output in BF16 instead of `out`, or null
+    int row_tiles;                     // of 128 rows per CTA, 1 or 2 (windowed calls)
 };
 
 // What the rows of query tokens [i0, i1] of a windowed call see of a sequence
@@ -65,13 +66,13 @@ cudaError_t launch_prefill(const PrefillArgs &a, int ba, int br, cudaStream_t st
 
 // Windowed attention of several new tokens (prefill_bf16.cu): over a BF16 cache,
 // k, v [B * H][Tp][d]; or over the rows that launch_rebuild wrote as `r` says,
-// then the tail, for the kv heads [r.h0, r.h0 + r.H).  a->nqb and a->S are the
-// plan's; record fields are unused.  With a->S > 1 launch_merge_rows follows.
+// then the tail, for the kv heads [r.h0, r.h0 + r.H).  a->row_tiles, a->nqb and
+// a->S are the plan's; record fields are unused.  With a->S > 1 launch_merge_rows follows.
 struct ReadArgs;
 void prefill_bf16_plan(PrefillArgs *a, int sms);
-cudaError_t launch_prefill_bf16(const PrefillArgs &a, const uint16_t *k, const uint16_t *v, const int *nonfinite, int sms,
+cudaError_t launch_prefill_bf16(const PrefillArgs &a, const uint16_t *k, const uint16_t *v, const int *nonfinite,
                                 cudaStream_t st);
-cudaError_t launch_prefill_rebuilt(const PrefillArgs &a, const ReadArgs &r, int sms, cudaStream_t st);
+cudaError_t launch_prefill_rebuilt(const PrefillArgs &a, const ReadArgs &r, cudaStream_t st);
 cudaError_t launch_merge_rows(const PrefillArgs &a, cudaStream_t st);
 
 }  // namespace rq

@@ -54,6 +54,7 @@
 #include <math_constants.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 
 #include "combine.cuh"
@@ -698,43 +699,60 @@ cudaError_t launch_rb(int qt, const Maps &m, const Bf16Args &a, cudaStream_t st)
     return a.out16 ? launch_t<2, false, RB>(m, a, st) : launch_t<2, true, RB>(m, a, st);
 }
 
-// Row tiles per CTA: two share their K and V tiles; one while there are no
-// more rows, or too few row blocks to fill the device with pairs.
-int row_tiles(const PrefillArgs &a, int sms) {
-    const long rows = (long)a.n * a.G, units = (long)a.B * a.H;
-    return rows <= kTileR || units * ((rows + 2 * kTileR - 1) / (2 * kTileR)) < sms ? 1 : 2;
+// How a call is cut: QT row tiles per CTA and S splits.  The time of the launch
+// is estimated in the time of one token tile of one row tile (about 1.1 us): a
+// CTA takes its tiles (two row tiles at once cost 1.7: 3700 against 2160 cycles)
+// and a fixed part of three (set-up, output).  If the CTAs do not fit the SMs at
+// once, it is their total over the SMs and what the uneven end leaves idle:
+// little where they differ in length, as the longest start first, and up to the
+// last, partly filled round where they do not.  Splits add a launch (four) and
+// their partials' way through memory (3.3 MB in that time): for a causal chunk
+// of 4096 tokens of 8 heads, 86 us with two splits and 51 with one.
+struct Cut {
+    int qt, S;
+};
+Cut choose_cut(const PrefillArgs &a, int sms) {
+    Cut best = {1, 1};
+    double best_cost = -1;
+    const int nq = a.n * a.G;
+    for (int qt = 1; qt <= (nq > kTileR ? 2 : 1); qt++) {
+        const int rows = kTileR * qt, nqb = (nq + rows - 1) / rows;
+        long total = 0;   // tiles of all row blocks of a kv head
+        int most = 1, least = 1 << 30;
+        for (int b = 0; b < a.B; b++)
+            for (int r0 = 0; r0 < nq; r0 += rows) {
+                const int t = Runs(a.seqT.v[b], a.n_tail, a.n, r0 / a.G, (std::min(r0 + rows, nq) - 1) / a.G, a.window, a.sinks).tiles;
+                total += t;
+                most = std::max(most, t);
+                least = std::min(least, t);
+            }
+        const double tile = qt == 2 ? 1.7 : 1.0, units = (double)a.B * a.H * nqb, same = (double)least / most;
+        for (int S = 1; S <= std::min(most, kMaxSplits); S++) {
+            const double fixed = 3, ctas = units * S;
+            const double longest = (most + S - 1) / S * tile + fixed;
+            const double mean = (double)total * a.H * tile / ctas + fixed;
+            double cost = longest;
+            if (ctas > sms) {
+                const double rounds = ctas / sms;
+                cost = std::max(cost, rounds * mean + (same * (std::ceil(rounds) - rounds) + (1 - same) * 0.25) * mean);
+            }
+            if (S > 1) cost += 4 + (double)a.B * nq * a.H * S * (2 * kPartialStride * sizeof(float)) / 3.3e6;
+            if (best_cost < 0 || cost < best_cost) {
+                best_cost = cost;
+                best = Cut{qt, S};
+            }
+        }
+    }
+    return best;
 }
 
 }  // namespace
 
 void prefill_bf16_plan(PrefillArgs *a, int sms) {
-    const int rows = kTileR * row_tiles(*a, sms), slots = sms;
-    const int nq = a->n * a->G;
-    a->nqb = (nq + rows - 1) / rows;
-    // tiles of all row blocks, and of the longest
-    long total = 0;
-    int nt = 1;
-    for (int b = 0; b < a->B; b++)
-        for (int r0 = 0; r0 < nq; r0 += rows) {
-            const int t = Runs(a->seqT.v[b], a->n_tail, a->n, r0 / a->G, (std::min(r0 + rows, nq) - 1) / a->G, a->window, a->sinks).tiles;
-            total += t;
-            nt = std::max(nt, t);
-        }
-    total *= a->H;
-    // In tiles' time: the work of all CTAs (set-up and output about two tiles
-    // each, the partials of a split another two) over the slots, and half of
-    // the longest CTA for the uneven end.
-    const long units = (long)a->B * a->H * a->nqb;
-    double best = -1;
-    for (int S = 1; S <= std::min(nt, kMaxSplits); S++) {
-        const int fixed = S > 1 ? 4 : 2;
-        const double longest = (nt + S - 1) / S + fixed;
-        const double cost = std::max((total + (double)units * S * fixed) / slots + 0.5 * longest, longest);
-        if (best < 0 || cost < best) {
-            best = cost;
-            a->S = S;
-        }
-    }
+    const Cut cut = choose_cut(*a, sms);
+    a->row_tiles = cut.qt;
+    a->S = cut.S;
+    a->nqb = (a->n * a->G + kTileR * cut.qt - 1) / (kTileR * cut.qt);
 }
 
 static Bf16Args bf16_args(const PrefillArgs &p, const int *nonfinite) {
@@ -762,16 +780,16 @@ static Bf16Args bf16_args(const PrefillArgs &p, const int *nonfinite) {
     return a;
 }
 
-cudaError_t launch_prefill_bf16(const PrefillArgs &p, const uint16_t *k, const uint16_t *v, const int *nonfinite, int sms,
+cudaError_t launch_prefill_bf16(const PrefillArgs &p, const uint16_t *k, const uint16_t *v, const int *nonfinite,
                                 cudaStream_t st) {
     Maps m;
     std::memset(&m, 0, sizeof(m));
     const long long heads = (long long)p.B * p.H;
     if (!make_map(&m.k, k, p.Tp, heads) || !make_map(&m.v, v, p.Tp, heads)) return cudaErrorInvalidValue;
-    return launch_rb<false>(row_tiles(p, sms), m, bf16_args(p, nonfinite), st);
+    return launch_rb<false>(p.row_tiles, m, bf16_args(p, nonfinite), st);
 }
 
-cudaError_t launch_prefill_rebuilt(const PrefillArgs &p, const ReadArgs &r, int sms, cudaStream_t st) {
+cudaError_t launch_prefill_rebuilt(const PrefillArgs &p, const ReadArgs &r, cudaStream_t st) {
     Maps m;
     std::memset(&m, 0, sizeof(m));
     const long long heads = (long long)p.B * r.H;
@@ -786,7 +804,7 @@ cudaError_t launch_prefill_rebuilt(const PrefillArgs &p, const ReadArgs &r, int 
     Bf16Args a = bf16_args(p, r.nonfinite);
     a.h0 = r.h0;
     a.heads = r.H;
-    return launch_rb<true>(row_tiles(p, sms), m, a, st);
+    return launch_rb<true>(p.row_tiles, m, a, st);
 }
 
 cudaError_t launch_merge_rows(const PrefillArgs &p, cudaStream_t st) {

@@ -232,11 +232,19 @@ __device__ __forceinline__ void pair_rest(const ReadArgs &a, const Span &s, cons
         store_pair(a, s.kv, pair_at(a, s, i) + 4 * lane, zero);
     if (s.kv == 1 && a.n_tail > 0) {
         const int spans = (a.pair_rows / kRecs + a.tiles - 1) / a.tiles, mine = s.tile0 / a.tiles;
+        const uint16_t *base = a.tail[1] + ((size_t)s.b * a.tail_cap * a.H_all + a.h0 + s.h) * kHeadDim + 4 * lane;
         uint32_t bad = 0;
-        for (int t = mine; t < a.n_tail; t += spans) {
-            const uint2 w = __ldcg(reinterpret_cast<const uint2 *>(
-                                       a.tail[1] + (((size_t)s.b * a.tail_cap + t) * a.H_all + a.h0 + s.h) * kHeadDim) + lane);
-            bad |= (((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u)) & 0x80008000u;
+        for (int t0 = mine; t0 < a.n_tail; t0 += 8 * spans) {   // eight rows in flight
+            uint2 w[8];
+#pragma unroll
+            for (int u = 0; u < 8; u++) {
+                const int t = t0 + u * spans;
+                w[u] = t < a.n_tail ? __ldcg(reinterpret_cast<const uint2 *>(base + (size_t)t * a.H_all * kHeadDim))
+                                    : make_uint2(0u, 0u);
+            }
+#pragma unroll
+            for (int u = 0; u < 8; u++)
+                bad |= (((w[u].x & 0x7F807F80u) + 0x00800080u) | ((w[u].y & 0x7F807F80u) + 0x00800080u)) & 0x80008000u;
         }
         if (bad) *a.nonfinite = 1;
     }
