@@ -185,10 +185,22 @@ def _ptr(t) -> int:
     return 0 if t is None else int(t.data_ptr())
 
 
+_raw_stream = None   # the current device's current stream as an integer; set by the first call
+
+
 def _stream(stream) -> int:
+    global _raw_stream
     if stream is None:
-        import torch
-        return int(torch.cuda.current_stream().cuda_stream)
+        if _raw_stream is None:
+            import torch
+            c = torch._C
+            torch.cuda.current_stream()   # initializes CUDA
+            # (a torch.cuda.Stream object costs 3 us a call, more than a launch)
+            if hasattr(c, "_cuda_getCurrentRawStream") and hasattr(c, "_cuda_getDevice"):
+                _raw_stream = lambda: c._cuda_getCurrentRawStream(c._cuda_getDevice())   # noqa: E731
+            else:
+                _raw_stream = lambda: int(torch.cuda.current_stream().cuda_stream)       # noqa: E731
+        return _raw_stream()
     return int(getattr(stream, "cuda_stream", stream))
 
 
@@ -269,20 +281,20 @@ def rq_decode_attn_noalloc(h, layer: int, loop: int, q, out, softmax_scale: floa
 
 def rq_decode_attn_window(h, layer: int, loop: int, q, out, out_type: int, softmax_scale: float, window: int,
                           sinks: int, stream=None) -> int:
-    return lib.rq_decode_attn_window(h, layer, loop, ctypes.c_void_p(_ptr(q)), ctypes.c_void_p(_ptr(out)), out_type,
-                                     softmax_scale, window, sinks, ctypes.c_void_p(_stream(stream)))
+    return lib.rq_decode_attn_window(h, layer, loop, _ptr(q), _ptr(out), out_type, softmax_scale, window, sinks,
+                                     _stream(stream))
 
 
 def rq_prefill_attn_window(h, layer: int, loop: int, q, n_tokens: int, out, out_type: int, softmax_scale: float,
                            window: int, sinks: int, stream=None) -> int:
-    return lib.rq_prefill_attn_window(h, layer, loop, ctypes.c_void_p(_ptr(q)), n_tokens, ctypes.c_void_p(_ptr(out)),
-                                      out_type, softmax_scale, window, sinks, ctypes.c_void_p(_stream(stream)))
+    return lib.rq_prefill_attn_window(h, layer, loop, _ptr(q), n_tokens, _ptr(out), out_type, softmax_scale, window,
+                                      sinks, _stream(stream))
 
 
 def rq_cache_read(h, layer: int, loop: int, t0: int, n_tokens: int, out_type: int, k, v, stride_b: int,
                   stride_t: int, stride_h: int, stream=None) -> int:
-    return lib.rq_cache_read(h, layer, loop, t0, n_tokens, out_type, ctypes.c_void_p(_ptr(k)),
-                             ctypes.c_void_p(_ptr(v)), stride_b, stride_t, stride_h, ctypes.c_void_p(_stream(stream)))
+    return lib.rq_cache_read(h, layer, loop, t0, n_tokens, out_type, _ptr(k), _ptr(v), stride_b, stride_t, stride_h,
+                             _stream(stream))
 
 
 def rq_cache_length(h, layer: int, group: int) -> int:
