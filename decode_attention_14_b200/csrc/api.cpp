@@ -954,10 +954,10 @@ int prefill_workspace(rq_cache *c, size_t floats, size_t units, cudaStream_t st)
 int plan_rebuild(rq_cache *c, const PrefillArgs &a, cudaStream_t st, ReadArgs *r) {
     int rows = 0;
     for (int b = 0; b < a.B; b++)
-        rows = std::max(rows, rebuilt_rows(a.seqT.v[b], a.n_tail, a.n, a.window, a.sinks).rows(a.seqT.v[b]));
+        rows = std::max(rows, rebuilt_rows(a.seqT.v[b] + a.n_tail, a.n, a.window, a.sinks).rows(a.seqT.v[b] + a.n_tail));
     rows = (rows + 15) / 16 * 16 + 128;   // a reader's tile may begin at the last row
     const size_t head = (size_t)a.B * rows * kHeadDim;   // elements of one part of one kv head
-    const int parts = a.out16 ? 3 : 4;                   // K high and low, V (high and low)
+    const int parts = a.out16 ? 2 : 4;                   // K and V; fp32 output: high and low
     const int heads = (int)std::min<size_t>(a.H, std::max<size_t>(1, kRebuildMax / (head * 2 * parts)));
     const size_t part = head * heads;
     if (part * 2 * parts > c->rebuild_bytes) {
@@ -987,10 +987,10 @@ int plan_rebuild(rq_cache *c, const PrefillArgs &a, cudaStream_t st, ReadArgs *r
     r->nr = a.r_codes[0] ? 1 : 0;
     r->tail[0] = a.tail_k;
     r->tail[1] = a.tail_v;
-    r->out[0] = c->rebuild_ws;
-    r->out_lo[0] = c->rebuild_ws + part;
-    r->out[1] = c->rebuild_ws + 2 * part;
-    r->out_lo[1] = parts == 4 ? c->rebuild_ws + 3 * part : nullptr;
+    for (int kv = 0; kv < 2; kv++) {
+        r->out[kv] = c->rebuild_ws + kv * part;
+        r->out_lo[kv] = parts == 4 ? c->rebuild_ws + (2 + kv) * part : nullptr;
+    }
     r->pair_stride = rows;
     r->pair_rows = rows;
     r->seqT = a.seqT;

@@ -655,7 +655,8 @@ __global__ void __launch_bounds__(kThreads, GK == 1 ? RQ_DECODE_MIN_CTAS : 3) de
     }
     consumer_sync();
     const float qmax = fmaxf(fmaxf(s_red[0][0], s_red[1][0]), fmaxf(s_red[2][0], s_red[3][0]));
-    const float qscale = fixed_scale(qmax, 22);  // q_int = round(q * qscale), |q_int| < 2^22
+    // q_int = round(q * qscale), |q_int| < 2^22 (WIN: at most 2^23 - 1; 16 codes of 15 times that fit an int)
+    const float qscale = fixed_scale(qmax, WIN ? 23 : 22);
     const float qinv = 1.f / qscale;             // exact (power of two)
     // Each consumer thread converts element tid of q (and of R q) and stores
     // its three bytes where the lanes of its segment pick them up as plane
@@ -667,7 +668,8 @@ __global__ void __launch_bounds__(kThreads, GK == 1 ? RQ_DECODE_MIN_CTAS : 3) de
         for (int gq = 0; gq < GK; gq++) {
 #pragma unroll
             for (int ab = 0; ab < (RESID ? 2 : 1); ab++) {
-                const int x = __float2int_rn(s_q[gq][ab][tid] * qscale);
+                int x = __float2int_rn(s_q[gq][ab][tid] * qscale);
+                if (WIN) x = min(x, (1 << 23) - 1);
                 uint8_t *dst = &s_qp[gq][ab][0][sg * 16 + (ab == 0 ? slot_of<BA>(i) : slot_of<BR>(i))];
                 dst[0] = (uint8_t)(x & 0xFF);
                 dst[kHeadDim] = (uint8_t)((x >> 8) & 0xFF);

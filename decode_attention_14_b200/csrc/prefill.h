@@ -38,24 +38,19 @@ struct PrefillArgs {
     int row_tiles;                     // of 128 rows per CTA, 1 or 2 (windowed calls)
 };
 
-// What the rows of query tokens [i0, i1] of a windowed call see of a sequence
-// of T committed and n_tail tail tokens: committed [0, sink_end) and [w_tile,
-// lim) (the first row's window begins at w0, in the 64 tokens from w_tile on),
-// tail tokens [tail0, tail1).
+// What the rows of query tokens [i0, i1] (of the n last) of a windowed call see
+// of a sequence of `end` tokens: positions [0, sink_end) and [w_tile, lim) (the
+// first row's window begins at w0, in the 64 positions from w_tile on).
 struct BlockRuns {
-    int sink_end, w_tile, w0, lim, tail0, tail1;
+    int sink_end, w_tile, w0, lim;
 };
-__host__ __device__ inline BlockRuns block_runs(int T, int n_tail, int n, int i0, int i1, int window, int sinks) {
+__host__ __device__ inline BlockRuns block_runs(int end, int n, int i0, int i1, int window, int sinks) {
     BlockRuns r;
-    const long long p0 = (long long)T + n_tail - n + i0, p1 = (long long)T + n_tail - n + i1;   // positions
-    const long long first = p0 + 1 - window;                                                    // of row i0's window
-    r.lim = (int)(p1 + 1 < T ? p1 + 1 : T);
-    r.w0 = (int)(first < 0 ? 0 : first > r.lim ? r.lim : first);
-    r.w_tile = r.w0 == r.lim ? r.lim : r.w0 / kTokTile * kTokTile;
+    const long long first = (long long)end - n + i0 + 1 - window;   // of row i0's window
+    r.lim = end - n + i1 + 1;
+    r.w0 = first < 0 ? 0 : (int)first;
+    r.w_tile = r.w0 / kTokTile * kTokTile;
     r.sink_end = sinks < r.w_tile ? sinks : r.w_tile;
-    r.tail1 = p1 + 1 > T ? (int)(p1 + 1 - T) : 0;
-    r.tail0 = first > T && sinks <= T ? (int)(first - T) / kPrefillTile * kPrefillTile : 0;
-    if (r.tail0 > r.tail1) r.tail0 = r.tail1;
     return r;
 }
 
@@ -66,7 +61,7 @@ cudaError_t launch_prefill(const PrefillArgs &a, int ba, int br, cudaStream_t st
 
 // Windowed attention of several new tokens (prefill_bf16.cu): over a BF16 cache,
 // k, v [B * H][Tp][d]; or over the rows that launch_rebuild wrote as `r` says,
-// then the tail, for the kv heads [r.h0, r.h0 + r.H).  a->row_tiles, a->nqb and
+// for the kv heads [r.h0, r.h0 + r.H).  a->row_tiles, a->nqb and
 // a->S are the plan's; record fields are unused.  With a->S > 1 launch_merge_rows follows.
 struct ReadArgs;
 void prefill_bf16_plan(PrefillArgs *a, int sms);

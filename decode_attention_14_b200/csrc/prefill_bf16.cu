@@ -12,10 +12,11 @@
 // row = query token x head of the group).  Per 128-token tile and 128 rows, on
 // the tcgen05 tensor cores:
 //   S = Q K^T   8 MMAs of 128x128x16, both operands from shared memory
-//   O += P V    8 MMAs of 128x128x16 with P from tensor memory (16 with SPLIT:
-//               P as a BF16 high and low part, relative 2^-17, for fp32 output;
-//               for BF16 output P is rounded to BF16, half a step of which,
-//               2^-9 of each weight, is as small as the output's own rounding)
+//   O += P V    8 MMAs of 128x128x16 with P from tensor memory, for each of P's
+//               PP BF16 parts: one for BF16 output (half a step, 2^-9 of each
+//               weight, is as small as the output's own rounding), a high and
+//               a low one for fp32 output (2^-17; a third one did not lower the
+//               3e-6 that the tensor cores' sums leave)
 // P overwrites S in tensor memory; O is beside it (128 columns each).  Two S
 // buffers keep the tensor cores and the softmax busy at once: with QT = 2 one
 // per row tile -- one tile's MMAs run while the other's softmax does, and both
@@ -37,12 +38,12 @@
 //             rescaled with QT = 1, and at the end)
 //
 // RB: the same over a compressed cache.  A first launch (rebuild.cu) writes the
-// committed tokens that the chunk sees as BF16 high and low parts into a
-// workspace, once for all the chunk's rows; then S = Q (Khi + Klo)^T, and for
-// fp32 output O += Phi Vhi + Plo Vhi + Phi Vlo (relative 2^-17).  For BF16
-// output V's low part is left out like P's: both round at random, half a step
-// each.  The tail's tokens are BF16 as they are; their tiles follow the
-// committed ones and have no low parts.
+// tokens that the chunk sees, committed and tail, as FP16 into a workspace, once
+// for all the chunk's rows, and every product is in FP16 with K and V scaled by
+// 2^-8 and q by 2^-4: for BF16 output one part each of K, V and P (2^-12, below
+// the output's own rounding), for fp32 output two: S = Q (Khi + Klo)^T,
+// O += (Phi + Plo) Vhi + Phi Vlo.  (In BF16 that takes two parts of K even for
+// BF16 output: 50 instead of 38 us, 768 instead of 512 workspace bytes a token.)
 //
 // A V row that only some rows see may hold NaN or infinities, which 0 * NaN
 // would carry into the other rows.  The store kernel notes in the arena when it
@@ -88,13 +89,6 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, int
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
         "[%5];" ::"r"(dst),
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-        : "memory");
-}
-__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-        "[%6];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
         : "memory");
 }
 __device__ __forceinline__ void expect_tx(uint64_t *bar, uint32_t bytes) {
@@ -152,6 +146,15 @@ __device__ __forceinline__ uint32_t pack_bf16(float x0, float x1) {   // x0 in t
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(x1), "f"(x0));
     return d;
 }
+__device__ __forceinline__ uint32_t pack_f16(float x0, float x1) {
+    const __half2 h = __floats2half2_rn(x0, x1);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2 *>(&w)); }
+constexpr float kQScale = 1.f / 16.f;   // of q in FP16: up to 1e6
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w) {
+    return pack_f16(__uint_as_float(w << 16) * kQScale, __uint_as_float(w & 0xFFFF0000u) * kQScale);
+}
 // bits [lo, hi) of a 32-bit word (clamped)
 __device__ __forceinline__ uint32_t range_bits(int lo, int hi) {
     lo = max(lo, 0);
@@ -167,39 +170,35 @@ struct Bf16Args {
     int *err;
     const int *nonfinite;   // a V that is not finite was ever stored
     SeqLens seqT;
-    int B, H, Hq, G, n, n_tail, S, nqb;
+    int B, H, Hq, G, n, n_tail, S, nqb;   // n_tail: tokens after the committed ones (RB)
     int h0;                 // RB: the launch's first kv head; z counts the launch's heads
     int heads;              // of the launch
     int window, sinks;
     float scale_log2;
 };
 
-// Tensor maps: K and V (their high parts under RB), the low parts, the tail's.
+// Tensor maps: K and V (RB: the rebuilt rows), and with two parts the low ones.
 struct Maps {
-    CUtensorMap k, v, k_lo, v_lo, tail_k, tail_v;
+    CUtensorMap k, v, k_lo, v_lo;
 };
 
-// The token runs that rows of query tokens [i0, i1] read, in tiles of 128: the
-// sinks', the window's, the tail's.
+// The token runs that rows of query tokens [i0, i1] read of a sequence of `end`
+// tokens, in tiles of 128: the sinks', the window's.
 struct Runs {
-    int sink_tiles, sink_end, w_tile, committed, tail0, tiles;
-    __host__ __device__ Runs(int T, int n_tail, int n, int i0, int i1, int window, int sinks) {
-        const BlockRuns r = block_runs(T, n_tail, n, i0, i1, window, sinks);
+    int sink_tiles, sink_end, w_tile, tiles;
+    __host__ __device__ Runs(int end, int n, int i0, int i1, int window, int sinks) {
+        const BlockRuns r = block_runs(end, n, i0, i1, window, sinks);
         w_tile = r.w_tile;
         sink_end = r.sink_end;
         sink_tiles = (r.sink_end + kTileT - 1) / kTileT;
-        committed = sink_tiles + (r.lim - r.w_tile + kTileT - 1) / kTileT;
-        tail0 = r.tail0;
-        tiles = committed + (r.tail1 - r.tail0 + kTileT - 1) / kTileT;
+        tiles = sink_tiles + (r.lim - r.w_tile + kTileT - 1) / kTileT;
     }
-    // first committed token of a tile below `committed`, first tail token of one from there on
     __host__ __device__ int token(int tile) const {
-        return tile < sink_tiles ? tile * kTileT
-                                 : tile < committed ? w_tile + (tile - sink_tiles) * kTileT : tail0 + (tile - committed) * kTileT;
+        return tile < sink_tiles ? tile * kTileT : w_tile + (tile - sink_tiles) * kTileT;
     }
 };
 
-template <int QT, bool SPLIT, bool RB>
+template <int QT, int PP, bool RB>
 __global__ void __launch_bounds__(Cfg<QT>::THREADS, 1)
     prefill_bf16_kernel(const __grid_constant__ Maps maps, const Bf16Args a) {
     using C = Cfg<QT>;
@@ -221,20 +220,18 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, 1)
     const int b = blockIdx.z / a.nqb, qb = a.nqb - 1 - blockIdx.z % a.nqb;   // the longest row blocks first
     const int r0 = qb * QT * kTileR;
     const int nr = min(QT * kTileR, a.n * a.G - r0);
-    const int Tb = a.seqT.v[b];
-    const Runs runs(Tb, a.n_tail, a.n, r0 / a.G, (r0 + nr - 1) / a.G, a.window, a.sinks);
+    const int Tb = a.seqT.v[b] + a.n_tail;   // tokens of the sequence
+    const Runs runs(Tb, a.n, r0 / a.G, (r0 + nr - 1) / a.G, a.window, a.sinks);
     // this split's tiles
     const int j0 = (int)((long long)split * runs.tiles / a.S), j1 = (int)((long long)(split + 1) * runs.tiles / a.S);
     const int nt = j1 - j0;
-    // Stages of tile j of the split: K, V -- or, of a rebuilt tile, K high and
-    // low, V (SPLIT: high and low); kstage / vstage are its first of each.
-    constexpr int CST = SPLIT ? 4 : 3;
-    const int nc = RB ? max(0, min(j1, runs.committed) - j0) : 0;   // rebuilt tiles
+    // stages of tile j of the split: K, V, under RB each in PP parts
+    constexpr int KP = RB ? PP : 1;
     // S buffer of row tile q's token tile j, and the parity of its phase then
     auto sbuf = [](int q, int j) { return QT == 2 ? q : j & 1; };
     auto sphase = [](int j) { return QT == 2 ? j & 1 : (j >> 1) & 1; };
-    auto kstage = [&](int j) { return RB ? (j <= nc ? CST * j : CST * nc + 2 * (j - nc)) : 2 * j; };
-    auto vstage = [&](int j) { return kstage(j) + (RB && j < nc ? 2 : 1); };
+    auto kstage = [](int j) { return 2 * KP * j; };
+    auto vstage = [](int j) { return 2 * KP * j + KP; };
 
     if (tid == 0) {
         for (int i = 0; i < NS; i++) {
@@ -260,6 +257,12 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, 1)
         if (row < nr) {
             const int rg = r0 + row, t = rg / a.G, gq = rg % a.G;
             v = __ldg(reinterpret_cast<const uint4 *>(a.q + (((size_t)b * a.n + t) * a.Hq + h * a.G + gq) * kHeadDim) + c);
+            if (RB) {   // FP16 times 2^-4
+                v.x = bf16x2_to_f16x2(v.x);
+                v.y = bf16x2_to_f16x2(v.y);
+                v.z = bf16x2_to_f16x2(v.z);
+                v.w = bf16x2_to_f16x2(v.w);
+            }
         }
         *reinterpret_cast<uint4 *>(sm + (row / kTileR) * kStageBytes + (c >> 3) * kBlkBytes +
                                    tc::sw_chunk(row % kTileR, c & 7)) = v;
@@ -284,37 +287,27 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, 1)
     if (warp == 4 * QT) {
         // ------------------------------------------------------- TMA
         if (lane == 0) {
-            const RebuiltRows rb = RB ? rebuilt_rows(Tb, a.n_tail, a.n, a.window, a.sinks) : RebuiltRows{0, 0};
+            const RebuiltRows rb = RB ? rebuilt_rows(Tb, a.n, a.window, a.sinks) : RebuiltRows{0, 0};
             int it = 0;
             bool ok = true;
-            // a K or V tile into the next stage: rows from y on of (sequence, head) z, or of the tail
-            auto load = [&](const CUtensorMap *map, int y, bool tail) {
+            // rows from y on of (sequence, head) z into the next stage
+            auto load = [&](const CUtensorMap *map, int y) {
                 const int s = it % NS;
                 if (ok && it >= NS) ok = wait(&bar_empty[s], (it / NS - 1) & 1, 31);
                 if (!ok) return;
                 const uint32_t dst = sstage + s * kStageBytes;
                 expect_tx(&bar_full[s], kStageBytes);
-                if (tail) {
-                    tma_4d(dst, map, 0, h, y, b, &bar_full[s]);
-                    tma_4d(dst + kBlkBytes, map, 64, h, y, b, &bar_full[s]);
-                } else {
-                    tma_3d(dst, map, 0, y, z, &bar_full[s]);
-                    tma_3d(dst + kBlkBytes, map, 64, y, z, &bar_full[s]);
-                }
+                tma_3d(dst, map, 0, y, z, &bar_full[s]);
+                tma_3d(dst + kBlkBytes, map, 64, y, z, &bar_full[s]);
                 it++;
             };
             for (int j = 0; j < nt && ok; j++) {
                 const int t = runs.token(j0 + j);
-                if (RB && j < nc) {
-                    const int y = j0 + j < runs.sink_tiles ? t : rb.sink_pad + t - rb.w_base;
-                    load(&maps.k, y, false);
-                    load(&maps.k_lo, y, false);
-                    load(&maps.v, y, false);
-                    if (SPLIT) load(&maps.v_lo, y, false);
-                } else {
-                    load(RB ? &maps.tail_k : &maps.k, t, RB);
-                    load(RB ? &maps.tail_v : &maps.v, t, RB);
-                }
+                const int y = RB && j0 + j >= runs.sink_tiles ? rb.sink_pad + t - rb.w_base : t;
+                load(&maps.k, y);
+                if (KP > 1) load(&maps.k_lo, y);
+                load(&maps.v, y);
+                if (KP > 1) load(&maps.v_lo, y);
             }
             // every issued load must have landed before the CTA exits
             for (int i = max(0, it - NS); i < it; i++) mbar_wait<256>(&bar_full[i % NS], (i / NS) & 1, abort_flag);
@@ -323,12 +316,14 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, 1)
     } else if (warp == 4 * QT + 1) {
         // ------------------------------------------------------- MMA
         if (lane == 0) {
-            constexpr uint32_t idS = tc::idesc_bf16(kTileR, kTileT, false);   // K: K-major
-            constexpr uint32_t idO = tc::idesc_bf16(kTileR, kHeadDim, true);  // V: MN-major
+            // (operand formats, bits 7-9 and 10-12: 1 BF16, 0 FP16)
+            constexpr uint32_t fmt = RB ? (1u << 7) | (1u << 10) : 0u;
+            constexpr uint32_t idS = tc::idesc_bf16(kTileR, kTileT, false) & ~fmt;    // K: K-major
+            constexpr uint32_t idO = tc::idesc_bf16(kTileR, kHeadDim, true) & ~fmt;   // V: MN-major
             auto logits = [&](int q, int j) {
                 const uint64_t da = tc::desc_k(sbase + q * kStageBytes);
-                const int parts = RB && j < nc ? 2 : 1;
-                for (int p = 0; p < parts; p++) {
+#pragma unroll
+                for (int p = 0; p < KP; p++) {
                     const int s = (kstage(j) + p) % NS;
                     const uint64_t db = tc::desc_k(sstage + s * kStageBytes);
 #pragma unroll
@@ -341,25 +336,24 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, 1)
                 tc::commit(&bar_sfull[sbuf(q, j)]);
             };
             auto values = [&](int q, int j) {
-                // (P part, V part): hi hi, lo hi, hi lo
-                const int terms = !SPLIT ? 1 : RB && j < nc ? 3 : 2;
+                // P's parts against V, then its high part against V's low one
+                constexpr int terms = PP + KP - 1;
+#pragma unroll
                 for (int p = 0; p < terms; p++) {
-                    const int s = (vstage(j) + (p == 2 ? 1 : 0)) % NS;
+                    const int s = (vstage(j) + (p == PP ? 1 : 0)) % NS;
                     const uint64_t dv = tc::desc_mn(sstage + s * kStageBytes, kBlkBytes);
-                    const uint32_t pa = tmem + sbuf(q, j) * 128 + (p == 1 ? 64 : 0);
+                    const uint32_t pa = tmem + sbuf(q, j) * 128 + (p == 1 && PP > 1 ? 64 : 0);
 #pragma unroll
                     for (int kk = 0; kk < 8; kk++)
                         mma_ts(tmem + 256 + q * 128, pa + kk * 8, dv + (uint64_t)((kk * 2048) >> 4), idO,
                                j > 0 || p > 0 || kk > 0);
-                    if (q == QT - 1 && (p == 2 || p == min(terms, 2) - 1)) tc::commit(&bar_empty[s]);
+                    if (q == QT - 1 && p >= PP - 1) tc::commit(&bar_empty[s]);
                 }
                 tc::commit(&bar_odone[q]);
             };
             auto loaded = [&](int i, int code) { return wait(&bar_full[i % NS], (i / NS) & 1, code); };
-            auto k_loaded = [&](int j) { return loaded(kstage(j), 32) && (!(RB && j < nc) || loaded(kstage(j) + 1, 33)); };
-            auto v_loaded = [&](int j) {
-                return loaded(vstage(j), 34) && (!(RB && SPLIT && j < nc) || loaded(vstage(j) + 1, 35));
-            };
+            auto k_loaded = [&](int j) { return loaded(kstage(j), 32) && (KP == 1 || loaded(kstage(j) + 1, 33)); };
+            auto v_loaded = [&](int j) { return loaded(vstage(j), 34) && (KP == 1 || loaded(vstage(j) + 1, 35)); };
             // logits run AHEAD tiles before values: with QT = 1 into the other S buffer
             constexpr int AHEAD = QT == 2 ? 1 : 2;
             bool ok = true;
@@ -390,18 +384,17 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, 1)
         const int q = warp >> 2;                       // row tile
         const int row = q * kTileR + (warp & 3) * 32 + lane;
         const bool live = q * kTileR + (warp & 3) * 32 < nr;   // warp-uniform: some row of the warp exists
-        const int pos = Tb + a.n_tail - a.n + (r0 + row) / a.G;   // the row's position
+        const int pos = Tb - a.n + (r0 + row) / a.G;   // the row's position
         const int lim = pos + 1;
         const int lo = (int)max(0ll, (long long)pos + 1 - a.window);
         const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16), tO = lanes + 256 + q * 128;
         const bool careful = __ldcg(a.nonfinite) != 0;
+        const float scale_log2 = RB ? a.scale_log2 * (1.f / (kQScale * kRebuildScale)) : a.scale_log2;
         float m_used = -CUDART_INF_F, l = 0.f;
         for (int j = 0; j < nt; j++) {
-            // positions tb .. of the tile's tokens; a sinks' tile may reach into the
-            // window's, a committed one (RB) past the sequence's committed tokens
-            const bool in_tail = j0 + j >= runs.committed;
-            const int tb = runs.token(j0 + j) + (in_tail ? Tb : 0);
-            const int end = j0 + j < runs.sink_tiles ? min(lim, runs.sink_end) : in_tail ? lim : min(lim, Tb);
+            const int tb = runs.token(j0 + j);
+            // a sinks' tile may reach into the window's: its part ends before that
+            const int end = j0 + j < runs.sink_tiles ? min(lim, runs.sink_end) : lim;
             const uint32_t tS = lanes + sbuf(q, j) * 128;
             wait(&bar_sfull[sbuf(q, j)], sphase(j), 38);
             tc::fence_after();
@@ -413,7 +406,7 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, 1)
                     const int s = vstage(j) % NS, t = tid;
                     wait(&bar_full[s], (vstage(j) / NS) & 1, 37);
                     const int s_lo = (vstage(j) + 1) % NS;
-                    const bool has_lo = RB && SPLIT && j < nc;
+                    constexpr bool has_lo = KP > 1;
                     if (has_lo) wait(&bar_full[s_lo], ((vstage(j) + 1) / NS) & 1, 37);
                     uint32_t bad = 0;
                     for (int c = 0; c < 16; c++) {
@@ -421,7 +414,8 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, 1)
                                                                          t * 128 + (c & 7) * 16);
                         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                        for (int i = 0; i < 4; i++) bad |= ((w[i] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+                        for (int i = 0; i < 4; i++)   // exponents all ones
+                            bad |= (RB ? (w[i] & 0x7C007C00u) + 0x04000400u : (w[i] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
                     }
                     if (bad)
                         for (int c = 0; c < (has_lo ? 32 : 16); c++)
@@ -462,7 +456,7 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, 1)
 #pragma unroll
                     for (int i = 0; i < 8; i++) m8[i] = fmaxf(m8[i], __uint_as_float(s[k + i]));
                 float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])), fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
-                mx *= a.scale_log2;
+                mx *= scale_log2;
                 const bool raise = mx > m_used + kRaiseLog2;   // false while nothing is seen
                 const bool rescale = raise && m_used != -CUDART_INF_F;
                 const float f = rescale ? exp2f(m_used - mx) : 1.f;
@@ -486,13 +480,13 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, 1)
                 }
                 l *= f;
                 const float off = m_used == -CUDART_INF_F ? 0.f : -m_used;
-                const F2 sc2 = pack2(a.scale_log2, a.scale_log2), off2 = pack2(off, off);
+                const F2 sc2 = pack2(scale_log2, scale_log2), off2 = pack2(off, off);
                 F2 sum[4];
 #pragma unroll
                 for (int k = 0; k < 4; k++) sum[k] = pack2(0.f, 0.f);
 #pragma unroll
                 for (int c = 0; c < 2; c++) {
-                    uint32_t hi[32], low[32];
+                    uint32_t hi[32], low[PP > 1 ? 32 : 1];
 #pragma unroll
                     for (int k = 0; k < 32; k++) {
                         const int u = 64 * c + 2 * k;
@@ -501,13 +495,16 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, 1)
                         p0 = ex2f(p0);
                         p1 = ex2f(p1);
                         sum[k & 3] = add2(sum[k & 3], pack2(p0, p1));
-                        hi[k] = pack_bf16(p0, p1);
-                        if (SPLIT)
-                            low[k] = pack_bf16(p0 - __uint_as_float(hi[k] << 16), p1 - __uint_as_float(hi[k] & 0xFFFF0000u));
+                        hi[k] = RB ? pack_f16(p0, p1) : pack_bf16(p0, p1);
+                        if (PP > 1) {
+                            const float2 f = RB ? unpack_f16(hi[k])
+                                                : make_float2(__uint_as_float(hi[k] << 16), __uint_as_float(hi[k] & 0xFFFF0000u));
+                            low[k] = RB ? pack_f16(p0 - f.x, p1 - f.y) : pack_bf16(p0 - f.x, p1 - f.y);
+                        }
                     }
                     __syncwarp();
                     st32(tS + 32 * c, hi);
-                    if (SPLIT) st32(tS + 64 + 32 * c, low);
+                    if (PP > 1) st32(tS + 64 + 32 * c, low);
                 }
                 float l0, l1;
                 unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), l0, l1);
@@ -530,7 +527,8 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, 1)
             const int rg = r0 + row, t = rg / a.G, gq = rg % a.G;
             const size_t prow = ((size_t)b * a.n + t) * a.Hq + h * a.G + gq;
             float *part = a.partials + (prow * a.S + split) * kPartialStride;
-            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const float back = RB ? 1.f / kRebuildScale : 1.f;   // O holds V's scale
+            const float inv = l == 0.f ? 0.f : back / l;
 #pragma unroll 1
             for (int c = 0; c < 4; c++) {
                 uint32_t v[32];
@@ -546,7 +544,9 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, 1)
                     if (a.S > 1) {
 #pragma unroll
                         for (int k = 0; k < 32; k += 4)
-                            *reinterpret_cast<uint4 *>(part + 32 * c + k) = make_uint4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                            *reinterpret_cast<float4 *>(part + 32 * c + k) =
+                                make_float4(__uint_as_float(v[k]) * back, __uint_as_float(v[k + 1]) * back,
+                                            __uint_as_float(v[k + 2]) * back, __uint_as_float(v[k + 3]) * back);
                     } else if (a.out16) {
 #pragma unroll
                         for (int k = 0; k < 32; k += 8) {
@@ -640,29 +640,17 @@ EncodeFn encode_fn() {
     return fn;
 }
 
-bool encode(CUtensorMap *map, const uint16_t *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
-            const cuuint32_t *box) {
+// [heads][rows][128] 16-bit numbers (a BF16 cache's K or V with rows = Tp, or
+// rebuilt rows in FP16): boxes of 128 rows x 64 elements, 128-byte swizzled;
+// rows past the last read as zeros.
+bool make_map(CUtensorMap *map, const void *base, bool f16, long long rows, long long heads) {
     const EncodeFn fn = encode_fn();
-    const cuuint32_t step[4] = {1, 1, 1, 1};
-    return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<uint16_t *>(base), dims, strides, box, step,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-// [heads][rows][128] BF16 (a BF16 cache's K or V with rows = Tp, or the rebuilt
-// rows): boxes of 128 rows x 64 elements, 128-byte swizzled; rows past the last
-// read as zeros.
-bool make_map(CUtensorMap *map, const uint16_t *base, long long rows, long long heads) {
     const cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)rows, (cuuint64_t)heads};
     const cuuint64_t strides[2] = {kHeadDim * 2, (cuuint64_t)rows * kHeadDim * 2};
-    const cuuint32_t box[3] = {64, kTileT, 1};
-    return encode(map, base, 3, dims, strides, box);
-}
-// The tail [B][cap][H][128]: the same boxes of one head.
-bool make_tail_map(CUtensorMap *map, const uint16_t *base, int B, int cap, int H) {
-    const cuuint64_t dims[4] = {(cuuint64_t)kHeadDim, (cuuint64_t)H, (cuuint64_t)cap, (cuuint64_t)B};
-    const cuuint64_t strides[3] = {kHeadDim * 2, (cuuint64_t)H * kHeadDim * 2, (cuuint64_t)cap * H * kHeadDim * 2};
-    const cuuint32_t box[4] = {64, 1, kTileT, 1};
-    return encode(map, base, 4, dims, strides, box);
+    const cuuint32_t box[3] = {64, kTileT, 1}, step[3] = {1, 1, 1};
+    return fn && fn(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base),
+                    dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // A launch that may begin while the one before it on the stream still runs.
@@ -682,21 +670,24 @@ cudaError_t launch_overlapped(void (*f)(P...), dim3 grid, int threads, int smem,
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int QT, bool SPLIT, bool RB>
+template <int QT, int PP, bool RB>
 cudaError_t launch_t(const Maps &m, const Bf16Args &a, cudaStream_t st) {
     static bool done[kMaxDevices];
     cudaError_t e = once_per_device(done, [] {
-        return cudaFuncSetAttribute(prefill_bf16_kernel<QT, SPLIT, RB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(prefill_bf16_kernel<QT, PP, RB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     Cfg<QT>::SMEM);
     });
     if (e != cudaSuccess) return e;
-    return launch_overlapped(prefill_bf16_kernel<QT, SPLIT, RB>, dim3(a.S, a.heads, a.B * a.nqb), Cfg<QT>::THREADS,
+    return launch_overlapped(prefill_bf16_kernel<QT, PP, RB>, dim3(a.S, a.heads, a.B * a.nqb), Cfg<QT>::THREADS,
                              Cfg<QT>::SMEM, RB, st, m, a);
 }
-template <bool RB>
-cudaError_t launch_rb(int qt, const Maps &m, const Bf16Args &a, cudaStream_t st) {
-    if (qt == 1) return a.out16 ? launch_t<1, false, RB>(m, a, st) : launch_t<1, true, RB>(m, a, st);
-    return a.out16 ? launch_t<2, false, RB>(m, a, st) : launch_t<2, true, RB>(m, a, st);
+cudaError_t launch_plain(int qt, const Maps &m, const Bf16Args &a, cudaStream_t st) {
+    if (qt == 1) return a.out16 ? launch_t<1, 1, false>(m, a, st) : launch_t<1, 2, false>(m, a, st);
+    return a.out16 ? launch_t<2, 1, false>(m, a, st) : launch_t<2, 2, false>(m, a, st);
+}
+cudaError_t launch_rebuilt(int qt, const Maps &m, const Bf16Args &a, cudaStream_t st) {
+    if (qt == 1) return a.out16 ? launch_t<1, 1, true>(m, a, st) : launch_t<1, 2, true>(m, a, st);
+    return a.out16 ? launch_t<2, 1, true>(m, a, st) : launch_t<2, 2, true>(m, a, st);
 }
 
 // How a call is cut: QT row tiles per CTA and S splits.  The time of the launch
@@ -721,7 +712,7 @@ Cut choose_cut(const PrefillArgs &a, int sms) {
         int most = 1, least = 1 << 30;
         for (int b = 0; b < a.B; b++)
             for (int r0 = 0; r0 < nq; r0 += rows) {
-                const int t = Runs(a.seqT.v[b], a.n_tail, a.n, r0 / a.G, (std::min(r0 + rows, nq) - 1) / a.G, a.window, a.sinks).tiles;
+                const int t = Runs(a.seqT.v[b] + a.n_tail, a.n, r0 / a.G, (std::min(r0 + rows, nq) - 1) / a.G, a.window, a.sinks).tiles;
                 total += t;
                 most = std::max(most, t);
                 least = std::min(least, t);
@@ -785,26 +776,22 @@ cudaError_t launch_prefill_bf16(const PrefillArgs &p, const uint16_t *k, const u
     Maps m;
     std::memset(&m, 0, sizeof(m));
     const long long heads = (long long)p.B * p.H;
-    if (!make_map(&m.k, k, p.Tp, heads) || !make_map(&m.v, v, p.Tp, heads)) return cudaErrorInvalidValue;
-    return launch_rb<false>(p.row_tiles, m, bf16_args(p, nonfinite), st);
+    if (!make_map(&m.k, k, false, p.Tp, heads) || !make_map(&m.v, v, false, p.Tp, heads)) return cudaErrorInvalidValue;
+    return launch_plain(p.row_tiles, m, bf16_args(p, nonfinite), st);
 }
 
 cudaError_t launch_prefill_rebuilt(const PrefillArgs &p, const ReadArgs &r, cudaStream_t st) {
     Maps m;
     std::memset(&m, 0, sizeof(m));
     const long long heads = (long long)p.B * r.H;
-    const bool lo = !p.out16;
-    if (!make_map(&m.k, static_cast<const uint16_t *>(r.out[0]), r.pair_stride, heads) ||
-        !make_map(&m.k_lo, r.out_lo[0], r.pair_stride, heads) ||
-        !make_map(&m.v, static_cast<const uint16_t *>(r.out[1]), r.pair_stride, heads) ||
-        (lo && !make_map(&m.v_lo, r.out_lo[1], r.pair_stride, heads)) ||
-        (p.n_tail > 0 && (!make_tail_map(&m.tail_k, p.tail_k, p.B, p.tail_cap, p.H) ||
-                          !make_tail_map(&m.tail_v, p.tail_v, p.B, p.tail_cap, p.H))))
+    if (!make_map(&m.k, r.out[0], true, r.pair_stride, heads) || !make_map(&m.v, r.out[1], true, r.pair_stride, heads) ||
+        (r.out_lo[0] && (!make_map(&m.k_lo, r.out_lo[0], true, r.pair_stride, heads) ||
+                         !make_map(&m.v_lo, r.out_lo[1], true, r.pair_stride, heads))))
         return cudaErrorInvalidValue;
     Bf16Args a = bf16_args(p, r.nonfinite);
     a.h0 = r.h0;
     a.heads = r.H;
-    return launch_rb<true>(p.row_tiles, m, a, st);
+    return launch_rebuilt(p.row_tiles, m, a, st);
 }
 
 cudaError_t launch_merge_rows(const PrefillArgs &p, cudaStream_t st) {

@@ -34,10 +34,11 @@
 // fp32 throughout (the codes, FP8 scales and minima are exact in it; two
 // elements per instruction), rounded once to the output's type.
 //
-// kOutPair (rebuild.cu) writes the rows that a chunk of new tokens attends to as
-// BF16 high and low parts (relative 2^-17 together) into a workspace, sequence
-// by sequence the rows that rebuilt_rows() names, for the tensor-core attention
-// of prefill_bf16.cu.
+// kOutPair (rebuild.cu) writes the rows that a chunk of new tokens attends to,
+// the tail's among them, as FP16 into a workspace for the tensor-core attention
+// of prefill_bf16.cu: one FP16 number each (2^-12) for BF16 output, a high and a
+// low one (2^-23) for fp32 output; sequence by sequence the rows that
+// rebuilt_rows() names.
 #pragma once
 
 #include "common.cuh"
@@ -209,45 +210,48 @@ __device__ __forceinline__ void expand4(const uint8_t *row, int sg, int q, float
 __device__ __forceinline__ long long pair_at(const ReadArgs &a, const Span &s, int i) {
     return (((long long)s.b * a.H + s.h) * a.pair_stride + i) * kHeadDim;
 }
-__device__ __forceinline__ void store_pair(const ReadArgs &a, int kv, long long at, const float (&x)[4]) {
-    uint32_t hi[2], lo[2];
+// Writes four values; nonzero if one of them is not finite (in FP16).
+__device__ __forceinline__ uint32_t store_pair(const ReadArgs &a, int kv, long long at, const float (&v)[4]) {
+    uint32_t hi[2], lo[2], bad = 0;
 #pragma unroll
     for (int k = 0; k < 2; k++) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
+        const float x0 = v[2 * k] * kRebuildScale, x1 = v[2 * k + 1] * kRebuildScale;
+        const __half2 h = __floats2half2_rn(x0, x1);
         hi[k] = *reinterpret_cast<const uint32_t *>(&h);
-        const __nv_bfloat162 l = __floats2bfloat162_rn(x[2 * k] - __uint_as_float(hi[k] << 16),
-                                                       x[2 * k + 1] - __uint_as_float(hi[k] & 0xFFFF0000u));
+        bad |= ((hi[k] & 0x7C007C00u) + 0x04000400u) & 0x80008000u;   // exponent all ones
+        const float2 f = __half22float2(h);
+        const __half2 l = __floats2half2_rn(x0 - f.x, x1 - f.y);
         lo[k] = *reinterpret_cast<const uint32_t *>(&l);
     }
     *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out[kv]) + at) = make_uint2(hi[0], hi[1]);
     if (a.out_lo[kv]) *reinterpret_cast<uint2 *>(a.out_lo[kv] + at) = make_uint2(lo[0], lo[1]);
+    return bad;
 }
-// What is left of the span beside the tiles with records: zero rows past the
-// sequence's end (a reader's tile of 128 rows ends there), and this warp's share
-// of looking the tail's V rows over for values that are not finite.
+// The span's rows beside those with records: the tail's tokens, and zero rows
+// past the sequence's end (a reader's tile of 128 rows ends there).
 __device__ __forceinline__ void pair_rest(const ReadArgs &a, const Span &s, const RebuiltRows &rb, int T, int lane) {
+    constexpr int kFly = 8;   // rows in flight
     const int end = min((s.tile0 + s.tiles) * kRecs, a.pair_rows);
-    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int i = max(s.tile0 * kRecs, (rb.rows(T) + kRecs - 1) / kRecs * kRecs); i < end; i++)
-        store_pair(a, s.kv, pair_at(a, s, i) + 4 * lane, zero);
-    if (s.kv == 1 && a.n_tail > 0) {
-        const int spans = (a.pair_rows / kRecs + a.tiles - 1) / a.tiles, mine = s.tile0 / a.tiles;
-        const uint16_t *base = a.tail[1] + ((size_t)s.b * a.tail_cap * a.H_all + a.h0 + s.h) * kHeadDim + 4 * lane;
-        uint32_t bad = 0;
-        for (int t0 = mine; t0 < a.n_tail; t0 += 8 * spans) {   // eight rows in flight
-            uint2 w[8];
+    const uint16_t *base =
+        a.n_tail > 0 ? a.tail[s.kv] + ((size_t)s.b * a.tail_cap * a.H_all + a.h0 + s.h) * kHeadDim + 4 * lane : nullptr;
+    uint32_t bad = 0;
+    for (int i0 = max(s.tile0 * kRecs, rb.rows(T)); i0 < end; i0 += kFly) {
+        uint2 w[kFly];
 #pragma unroll
-            for (int u = 0; u < 8; u++) {
-                const int t = t0 + u * spans;
-                w[u] = t < a.n_tail ? __ldcg(reinterpret_cast<const uint2 *>(base + (size_t)t * a.H_all * kHeadDim))
-                                    : make_uint2(0u, 0u);
-            }
-#pragma unroll
-            for (int u = 0; u < 8; u++)
-                bad |= (((w[u].x & 0x7F807F80u) + 0x00800080u) | ((w[u].y & 0x7F807F80u) + 0x00800080u)) & 0x80008000u;
+        for (int u = 0; u < kFly; u++) {
+            const int j = rb.position(i0 + u) - T;
+            w[u] = j < a.n_tail && i0 + u < end
+                       ? __ldcg(reinterpret_cast<const uint2 *>(base + (size_t)j * a.H_all * kHeadDim))
+                       : make_uint2(0u, 0u);
         }
-        if (bad) *a.nonfinite = 1;
+#pragma unroll
+        for (int u = 0; u < kFly; u++) {
+            const float x[4] = {__uint_as_float(w[u].x << 16), __uint_as_float(w[u].x & 0xFFFF0000u),
+                                __uint_as_float(w[u].y << 16), __uint_as_float(w[u].y & 0xFFFF0000u)};
+            if (i0 + u < end) bad |= store_pair(a, s.kv, pair_at(a, s, i0 + u) + 4 * lane, x);
+        }
     }
+    if (s.kv == 1 && bad) *a.nonfinite = 1;
 }
 
 // NR: residual records read, 0 or 1 (the shared reference), or 2 for any
@@ -271,7 +275,7 @@ __global__ void __launch_bounds__(32 * kWarps, NR == 2 ? 3 : RQ_READ_CTAS) read_
     RebuiltRows rb = {0, 0};
     if (OUT == kOutPair) {
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the attention may set itself up meanwhile
-        rb = rebuilt_rows(T, a.n_tail, a.n, a.window, a.sinks);
+        rb = rebuilt_rows(T + a.n_tail, a.n, a.window, a.sinks);
         pair_rest(a, sp, rb, T, lane);
         lo = 0;
         mid = T;
@@ -287,7 +291,7 @@ __global__ void __launch_bounds__(32 * kWarps, NR == 2 ? 3 : RQ_READ_CTAS) read_
         if (mid <= lo) return;
     }
     // first token of tile i of the span
-    auto tile_tok = [&](int i) { return OUT == kOutPair ? rb.token((sp.tile0 + i) * kRecs) : (sp.tile0 + i) * kRecs; };
+    auto tile_tok = [&](int i) { return OUT == kOutPair ? rb.position((sp.tile0 + i) * kRecs) : (sp.tile0 + i) * kRecs; };
 
     uint8_t *ring = smem + (threadIdx.x >> 5) * (kSlots * S::BYTES);
     const uint32_t ring_s = smem_u32(ring);
@@ -364,7 +368,7 @@ __global__ void __launch_bounds__(32 * kWarps, NR == 2 ? 3 : RQ_READ_CTAS) read_
     // x <- s_k x + R^T y_k unrolled, so that the anchor gets the product of
     // all of them and R^T is applied once.  Under ROT z holds H_16 z_g.
     int cs = 0;   // slot consumed
-    float finite = 0.f;
+    uint32_t bad = 0;   // kOutPair: a value is not finite
 #pragma unroll 1
     for (int tile = 0; tile < tiles; tile++) {
         F2 z[2][8][2];
@@ -478,13 +482,8 @@ __global__ void __launch_bounds__(32 * kWarps, NR == 2 ? 3 : RQ_READ_CTAS) read_
                 float o[4];
                 unpack2(x[0], o[0], o[1]);
                 unpack2(x[1], o[2], o[3]);
-                if (OUT == kOutPair) {   // zeros past the sequence's end
-                    float z[4];
-#pragma unroll
-                    for (int e = 0; e < 4; e++) z[e] = in[u] ? o[e] : 0.f;
-                    store_pair(a, sp.kv, at[u] + 16 * sg, z);
-#pragma unroll
-                    for (int e = 0; e < 4; e++) finite = fmaf(z[e], 0.f, finite);   // NaN from infinities and NaN
+                if (OUT == kOutPair) {
+                    if (in[u]) bad |= store_pair(a, sp.kv, at[u] + 16 * sg, o);
                 } else if (in[u]) {
                     store4<OUT>(a.out[sp.kv], at[u] + 16 * sg, o);
                 }
@@ -497,7 +496,7 @@ __global__ void __launch_bounds__(32 * kWarps, NR == 2 ? 3 : RQ_READ_CTAS) read_
         cs = cs + 1 == kSlots ? 0 : cs + 1;
     }
     async_wait<0>();
-    if (OUT == kOutPair && sp.kv == 1 && finite != 0.f) *a.nonfinite = 1;   // (NaN compares unequal)
+    if (OUT == kOutPair && sp.kv == 1 && bad) *a.nonfinite = 1;
 }
 
 template <int BA, int BR, int GS, int NR, bool ROT, int OUT>

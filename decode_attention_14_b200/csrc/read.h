@@ -28,12 +28,12 @@ struct ReadArgs {
     int g;
     int rotate;
     uint32_t sigma[4];
-    // launch_rebuild: `out` holds the high parts [B * H][pair_stride][d] BF16,
-    // out_lo the low parts (null: not wanted); pair_rows rows (a multiple of
-    // 16) of every sequence are written, zeros past its rebuilt ones; n, n_tail,
-    // window and sinks are the attention call's.  *nonfinite is set to 1 when a
-    // V value (the tail's among them) is not finite.
-    // The kv heads are [h0, h0 + H) of H_all.
+    // launch_rebuild: FP16 rows times kRebuildScale, `out` [B * H][pair_stride][d]
+    // (their high parts where out_lo takes the low ones); pair_rows rows (a
+    // multiple of 16) of every sequence are written, zeros past its rebuilt
+    // ones; n, n_tail, window and sinks are the attention call's.  *nonfinite is
+    // set to 1 when a V value is not finite in FP16.  The kv heads are
+    // [h0, h0 + H) of H_all.
     uint16_t *out_lo[2];
     int h0, H_all;
     long long pair_stride;
@@ -42,19 +42,24 @@ struct ReadArgs {
     int *nonfinite;
 };
 
-// The committed tokens that n new tokens of a windowed call see between them:
-// the sinks (rows 0 .. sink_pad - 1 of the workspace, whole tiles of 16), then
-// tokens w_base .. T - 1.
+// FP16 holds the rebuilt values times 2^-8: up to 1.6e7, with 11 bits down to
+// 0.016 and steps of 1.5e-5 below.
+constexpr float kRebuildScale = 1.f / 256.f;
+
+// The positions that n new tokens of a windowed call see between them, of a
+// sequence of `end` tokens: the sinks (rows 0 .. sink_pad - 1 of the workspace,
+// whole tiles of 16), then positions w_base .. end - 1.
 struct RebuiltRows {
     int sink_pad, w_base;
-    __host__ __device__ int rows(int T) const { return sink_pad + (T > w_base ? T - w_base : 0); }
-    __host__ __device__ int token(int row) const { return row < sink_pad ? row : row - sink_pad + w_base; }
+    // rows of the positions below p
+    __host__ __device__ int rows(int p) const { return p <= sink_pad ? p : sink_pad + (p > w_base ? p - w_base : 0); }
+    __host__ __device__ int position(int row) const { return row < sink_pad ? row : row - sink_pad + w_base; }
 };
-__host__ __device__ inline RebuiltRows rebuilt_rows(int T, int n_tail, int n, int window, int sinks) {
-    const long long first = (long long)T + n_tail - n + 1 - window;   // of the first row's window
-    const int base = first <= 0 ? 0 : first >= T ? (T + kTokTile - 1) / kTokTile * kTokTile : (int)(first / kTokTile * kTokTile);
+__host__ __device__ inline RebuiltRows rebuilt_rows(int end, int n, int window, int sinks) {
+    const long long first = (long long)end - n + 1 - window;   // of the first row's window
+    const int base = first <= 0 ? 0 : (int)(first / kTokTile * kTokTile);
     if (sinks > base) return RebuiltRows{0, 0};   // no gap between them
-    return RebuiltRows{((sinks < T ? sinks : T) + 15) / 16 * 16, base};
+    return RebuiltRows{(sinks + 15) / 16 * 16, base};
 }
 
 cudaError_t launch_rebuild(const ReadArgs &a, int ba, int br, cudaStream_t st);

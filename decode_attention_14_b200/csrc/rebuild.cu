@@ -1,6 +1,6 @@
 // rebuild.cu -- the rows that a chunk of new tokens attends to, rebuilt from the
-// compressed cache as BF16 pairs in a workspace (first half of
-// rq_prefill_attn_window on chunks of many rows): the kOutPair instantiations
+// compressed cache in FP16 in a workspace (the first launch of
+// rq_prefill_attn_window): the kOutPair instantiations
 // of read.cuh.
 #include "read.cuh"
 
