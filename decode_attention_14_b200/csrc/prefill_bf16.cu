@@ -433,11 +433,12 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, 1)
                 wait_ld32(s);
 #pragma unroll
                 for (int c = 1; c < 4; c++) settle32(s + 32 * c);
-                if (tb + kTileT > end || (tb < lo && tb + kTileT > a.sinks)) {   // an edge lies in the tile
+                if (__any_sync(0xffffffffu, tb + kTileT > end || (tb < lo && tb + kTileT > a.sinks))) {   // an edge lies in the tile
 #pragma unroll
                     for (int c = 0; c < 4; c++) {
                         const int p = tb + 32 * c;
                         const uint32_t vis = range_bits(0, end - p) & (range_bits(lo - p, 32) | range_bits(0, a.sinks - p));
+                        if (__all_sync(0xffffffffu, vis == 0xFFFFFFFFu)) continue;   // uniform
 #pragma unroll
                         for (int k = 0; k < 32; k++)
                             if (!((vis >> k) & 1u)) s[32 * c + k] = 0xFF800000u;   // -inf

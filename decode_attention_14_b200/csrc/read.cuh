@@ -78,9 +78,12 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 // set-up and overlap, as long as four rounds of the 16 warps an SM holds remain
 // to even out the end: at 8k b4 (residual) 99 / 104 / 119 us with 4 / 2 / 1, at
 // 15 000 tiles 24.4 / 21.1 / 21.2 us.
+#ifndef RQ_ROUNDS
+#define RQ_ROUNDS 4
+#endif
 inline int warp_tiles(long long tiles) {
     int per = kTiles;
-    while (per > 1 && tiles < 148LL * 16 * 4 * per) per /= 2;
+    while (per > 1 && tiles < 148LL * 16 * RQ_ROUNDS * per) per /= 2;
     return per;
 }
 
@@ -210,22 +213,19 @@ __device__ __forceinline__ void expand4(const uint8_t *row, int sg, int q, float
 __device__ __forceinline__ long long pair_at(const ReadArgs &a, const Span &s, int i) {
     return (((long long)s.b * a.H + s.h) * a.pair_stride + i) * kHeadDim;
 }
-// Writes four values; nonzero if one of them is not finite (in FP16).
+// Writes four values; nonzero if one of them is a V that is not finite (in FP16).
 __device__ __forceinline__ uint32_t store_pair(const ReadArgs &a, int kv, long long at, const float (&v)[4]) {
-    uint32_t hi[2], lo[2], bad = 0;
-#pragma unroll
-    for (int k = 0; k < 2; k++) {
-        const float x0 = v[2 * k] * kRebuildScale, x1 = v[2 * k + 1] * kRebuildScale;
-        const __half2 h = __floats2half2_rn(x0, x1);
-        hi[k] = *reinterpret_cast<const uint32_t *>(&h);
-        bad |= ((hi[k] & 0x7C007C00u) + 0x04000400u) & 0x80008000u;   // exponent all ones
-        const float2 f = __half22float2(h);
-        const __half2 l = __floats2half2_rn(x0 - f.x, x1 - f.y);
-        lo[k] = *reinterpret_cast<const uint32_t *>(&l);
+    const float x[4] = {v[0] * kRebuildScale, v[1] * kRebuildScale, v[2] * kRebuildScale, v[3] * kRebuildScale};
+    const __half2 h0 = __floats2half2_rn(x[0], x[1]), h1 = __floats2half2_rn(x[2], x[3]);
+    const uint2 hi = make_uint2(*reinterpret_cast<const uint32_t *>(&h0), *reinterpret_cast<const uint32_t *>(&h1));
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out[kv]) + at) = hi;
+    if (a.out_lo[kv]) {   // uniform
+        const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
+        const __half2 l0 = __floats2half2_rn(x[0] - f0.x, x[1] - f0.y), l1 = __floats2half2_rn(x[2] - f1.x, x[3] - f1.y);
+        *reinterpret_cast<uint2 *>(a.out_lo[kv] + at) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&l0), *reinterpret_cast<const uint32_t *>(&l1));
     }
-    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out[kv]) + at) = make_uint2(hi[0], hi[1]);
-    if (a.out_lo[kv]) *reinterpret_cast<uint2 *>(a.out_lo[kv] + at) = make_uint2(lo[0], lo[1]);
-    return bad;
+    return kv == 0 ? 0u : (((hi.x & 0x7C007C00u) + 0x04000400u) | ((hi.y & 0x7C007C00u) + 0x04000400u)) & 0x80008000u;
 }
 // The span's rows beside those with records: the tail's tokens, and zero rows
 // past the sequence's end (a reader's tile of 128 rows ends there).
