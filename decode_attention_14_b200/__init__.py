@@ -410,6 +410,7 @@ class Cache:
         shape = (self.B, self.Hq, HEAD_DIM)
         _check_dev(q, "bfloat16", shape, "q")
         out = self._window_out(out, dtype, shape, q)
+        self._on_device(q, out)
         _ok(rq_decode_attn_window(self.h, layer, loop, q, out, _out_type(out.dtype), scale, window, sinks, stream),
             "rq_decode_attn_window")
         return out
@@ -445,6 +446,7 @@ class Cache:
         shape = (self.B, n, self.Hq, HEAD_DIM)
         _check_dev(q, "bfloat16", shape, "q")
         out = self._window_out(out, dtype, shape, q)
+        self._on_device(q, out)
         _ok(rq_prefill_attn_window(self.h, layer, loop, q, n, out, _out_type(out.dtype), scale, window, sinks, stream),
             "rq_prefill_attn_window")
         return out
@@ -462,6 +464,11 @@ class Cache:
         _check_dev(out, "float32", (self.B, self.Hq, HEAD_DIM), "out")
         _ok(rq_append_decode_attn(self.h, layer, loop, k, v, n, q, out, scale, stream), "rq_append_decode_attn")
         return out
+
+    def _on_device(self, *tensors) -> None:
+        for t in tensors:
+            if t.device != self.device:
+                raise ValueError(f"a tensor on {t.device}, the cache is on {self.device}")
 
     def read(self, layer: int, loop: int, t0: int = 0, n: int | None = None, k=None, v=None, dtype=None,
              stream=None):
@@ -483,6 +490,7 @@ class Cache:
             k, v = (torch.zeros(shape, dtype=dtype or torch.bfloat16, device=self.device) for _ in range(2))
         for x, what in ((k, "k"), (v, "v")):
             _check_rows(x, (self.B, n, self.H, HEAD_DIM), what)
+        self._on_device(k, v)
         if k.dtype != v.dtype or (dtype is not None and k.dtype != dtype):
             raise ValueError(f"k and v must have one type{'' if dtype is None else f', {dtype}'}")
         if k.stride() != v.stride():

@@ -35,14 +35,18 @@ struct rq_cache {
     int occ[kMaxChain + 1][kMaxChunk / kTokTile];
     // split partials of rq_prefill_attn, allocated on first use and grown on demand
     float *prefill_ws = nullptr;
-    size_t prefill_ws_floats = 0;
+    size_t prefill_ws_bytes = 0;
     // arrival counters of rq_prefill_attn's row blocks (zeroed once; every
     // launch leaves them at zero)
     int *prefill_cnt = nullptr;
-    size_t prefill_cnt_n = 0;
+    size_t prefill_cnt_bytes = 0;
     // rebuilt rows of rq_prefill_attn_window's long chunks, likewise
     uint16_t *rebuild_ws = nullptr;
     size_t rebuild_bytes = 0;
+    // a call that uses these buffers was captured into a graph; buffers that
+    // were outgrown after that, freed with the cache
+    bool captured = false;
+    std::vector<void *> retired;
     // paged records: host copy of the block table [B][MB] (-1: no block),
     // reference counts of the physical blocks (forked sequences share
     // blocks), and the free list (blocks are taken from its back)
@@ -587,6 +591,7 @@ int rq_cache_destroy(rq_cache *c) {
     if (c->prefill_ws) cudaFree(c->prefill_ws);
     if (c->prefill_cnt) cudaFree(c->prefill_cnt);
     if (c->rebuild_ws) cudaFree(c->rebuild_ws);
+    for (void *p : c->retired) cudaFree(p);
     delete c;
     return st;
 }
@@ -905,47 +910,53 @@ bool capturing(cudaStream_t st) {
     return st && cudaStreamIsCapturing(st, &cap) == cudaSuccess && cap != cudaStreamCaptureStatusNone;
 }
 
-// Room for `floats` split partials and `units` arrival counters of the
-// multi-token attention, kept by the cache and grown on demand.
-// While `st` is being captured nothing can be allocated: NOMEM, the capture
-// left valid.
-int prefill_workspace(rq_cache *c, size_t floats, size_t units, cudaStream_t st) {
-    if ((floats > c->prefill_ws_floats || units > c->prefill_cnt_n) && capturing(st)) return RQ_ERR_NOMEM;
-    if (floats > c->prefill_ws_floats) {
-        if (c->prefill_ws) {
+// Makes *p a device buffer of at least `need` bytes (*have: its size), kept by
+// the cache and grown on demand.  Growing synchronises the device, unless a
+// captured graph may hold the old buffer: that is kept until the cache is
+// destroyed.  While `st` is being captured nothing can be allocated: NOMEM, the
+// capture left valid.
+int grow_buffer(rq_cache *c, void **p, size_t *have, size_t need, cudaStream_t st) {
+    const bool cap = capturing(st);
+    if (need > *have) {
+        if (cap) return RQ_ERR_NOMEM;
+        void *q = nullptr;
+        if (*p && !c->captured) {   // freed first, so that both need not fit at once
             if (cudaDeviceSynchronize() != cudaSuccess) return RQ_ERR_CUDA;
-            cudaFree(c->prefill_ws);
-            c->prefill_ws = nullptr;
-            c->prefill_ws_floats = 0;
+            cudaFree(*p);
+            *p = nullptr;
+            *have = 0;
         }
-        void *p = nullptr;
-        if (cudaMalloc(&p, floats * sizeof(float)) != cudaSuccess) {
+        if (cudaMalloc(&q, need) != cudaSuccess) {
             cudaGetLastError();
             return RQ_ERR_NOMEM;
         }
-        c->prefill_ws = (float *)p;
-        c->prefill_ws_floats = floats;
+        if (*p) {
+            try {
+                c->retired.push_back(*p);
+            } catch (...) {
+                cudaFree(q);
+                return RQ_ERR_NOMEM;
+            }
+        }
+        *p = q;
+        *have = need;
     }
-    if (units > c->prefill_cnt_n) {
-        if (c->prefill_cnt) {
-            if (cudaDeviceSynchronize() != cudaSuccess) return RQ_ERR_CUDA;
-            cudaFree(c->prefill_cnt);
-            c->prefill_cnt = nullptr;
-            c->prefill_cnt_n = 0;
-        }
-        void *p = nullptr;
-        if (cudaMalloc(&p, units * sizeof(int)) != cudaSuccess) {
-            cudaGetLastError();
-            return RQ_ERR_NOMEM;
-        }
-        if (cudaMemset(p, 0, units * sizeof(int)) != cudaSuccess) {
-            cudaFree(p);
-            return RQ_ERR_CUDA;
-        }
-        c->prefill_cnt = (int *)p;
-        c->prefill_cnt_n = units;
-    }
+    if (cap && need > 0) c->captured = true;
     return RQ_OK;
+}
+
+// Room for `floats` split partials and `units` arrival counters (zero when
+// allocated) of the multi-token attention.
+int prefill_workspace(rq_cache *c, size_t floats, size_t units, cudaStream_t st) {
+    if (units * sizeof(int) > c->prefill_cnt_bytes && capturing(st)) return RQ_ERR_NOMEM;
+    int s = grow_buffer(c, (void **)&c->prefill_ws, &c->prefill_ws_bytes, floats * sizeof(float), st);
+    if (s != RQ_OK) return s;
+    const size_t had = c->prefill_cnt_bytes;
+    s = grow_buffer(c, (void **)&c->prefill_cnt, &c->prefill_cnt_bytes, units * sizeof(int), st);
+    if (s == RQ_OK && c->prefill_cnt_bytes != had &&
+        cudaMemsetAsync(c->prefill_cnt, 0, c->prefill_cnt_bytes, st) != cudaSuccess)
+        return RQ_ERR_CUDA;
+    return s;
 }
 
 // The first launch of a windowed chunk over the compressed cache (rebuild.cu):
@@ -960,22 +971,8 @@ int plan_rebuild(rq_cache *c, const PrefillArgs &a, cudaStream_t st, ReadArgs *r
     const int parts = a.out16 ? 2 : 4;                   // K and V; fp32 output: high and low
     const int heads = (int)std::min<size_t>(a.H, std::max<size_t>(1, kRebuildMax / (head * 2 * parts)));
     const size_t part = head * heads;
-    if (part * 2 * parts > c->rebuild_bytes) {
-        if (capturing(st)) return RQ_ERR_NOMEM;
-        if (c->rebuild_ws) {
-            if (cudaDeviceSynchronize() != cudaSuccess) return RQ_ERR_CUDA;
-            cudaFree(c->rebuild_ws);
-            c->rebuild_ws = nullptr;
-            c->rebuild_bytes = 0;
-        }
-        void *p = nullptr;
-        if (cudaMalloc(&p, part * 2 * parts) != cudaSuccess) {
-            cudaGetLastError();
-            return RQ_ERR_NOMEM;
-        }
-        c->rebuild_ws = (uint16_t *)p;
-        c->rebuild_bytes = part * 2 * parts;
-    }
+    const int s = grow_buffer(c, (void **)&c->rebuild_ws, &c->rebuild_bytes, part * 2 * parts, st);
+    if (s != RQ_OK) return s;
     std::memset(r, 0, sizeof(*r));
     for (int kv = 0; kv < 2; kv++) {
         r->a_codes[kv] = a.a_codes[kv];
@@ -1409,18 +1406,18 @@ int rq_check(rq_cache *c) {
         // happened.
         cudaMemset(c->base + c->lay.off_counters, 0, c->lay.off_err + sizeof(int) - c->lay.off_counters);
         noalloc_reset_counters();
-        if (c->prefill_cnt) cudaMemset(c->prefill_cnt, 0, c->prefill_cnt_n * sizeof(int));
+        if (c->prefill_cnt) cudaMemset(c->prefill_cnt, 0, c->prefill_cnt_bytes);
         if (cudaDeviceSynchronize() != cudaSuccess) return RQ_ERR_CUDA;
         return RQ_ERR_TIMEOUT;
     }
     // every completed rq_prefill_attn leaves its split-arrival counters at zero
     if (c->prefill_cnt) {
-        std::vector<int> cnt(c->prefill_cnt_n);
+        std::vector<int> cnt(c->prefill_cnt_bytes / sizeof(int));
         if (cudaMemcpy(cnt.data(), c->prefill_cnt, cnt.size() * sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
             return RQ_ERR_CUDA;
         for (int v : cnt) {
             if (v != 0) {
-                cudaMemset(c->prefill_cnt, 0, c->prefill_cnt_n * sizeof(int));
+                cudaMemset(c->prefill_cnt, 0, c->prefill_cnt_bytes);
                 if (cudaDeviceSynchronize() != cudaSuccess) return RQ_ERR_CUDA;
                 return RQ_ERR_STATE;
             }

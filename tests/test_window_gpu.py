@@ -579,3 +579,60 @@ def test_prefill_window_beyond_one_workspace():
         assert np.linalg.norm(g_h - r_h) <= 1e-3 * np.linalg.norm(r_h) and np.abs(g_h - r_h).max() <= 2e-3, h
     cache.check()
     cache.close()
+
+
+@pytest.mark.parametrize("fmt", [rq.RQ_FMT_RESIDUAL, rq.RQ_FMT_BF16])
+def test_a_captured_call_outlives_a_larger_one(fmt):
+    """The buffers that a captured graph uses stay when a later, larger call outgrows them; so do rq_prefill_attn's."""
+    Lg = 4 if fmt == rq.RQ_FMT_RESIDUAL else 1
+    bt = H.build(loops=Lg, Lg=Lg, T=3000, H=2, Hq=4, fmt=fmt, seed=0x5EEDEE01)
+    q = queries(18, 1, 300, 4, 128)
+    small, out, loop = q[:, -2:].contiguous(), torch.zeros((1, 2, 4, 128), device="cuda"), Lg - 1
+    plain = [torch.zeros_like(out)] if Lg == 4 else []
+    first = bt.cache.prefill_window(0, loop, small, 600, 4)
+    ref = [bt.cache.prefill(0, loop, small) for _ in plain]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        bt.cache.prefill_window(0, loop, small, 600, 4, out=out)
+        for p in plain:
+            bt.cache.prefill(0, loop, small, out=p)
+    big = bt.cache.prefill_window(0, loop, q, 0)                 # more splits, more rebuilt rows
+    if plain:
+        bt.cache.prefill(0, loop, q)
+    junk = [torch.full((1 << 20,), 7.0, device="cuda") for _ in range(32)]     # would land in freed buffers
+    for _ in range(2):
+        out.zero_()
+        g.replay()
+        assert torch.equal(out, first) and all(torch.equal(p, r) for p, r in zip(plain, ref))
+    assert torch.equal(bt.cache.prefill_window(0, loop, q, 0), big)
+    del junk, g
+    bt.cache.check()
+    bt.cache.close()
+
+
+@pytest.mark.parametrize("fmt", [rq.RQ_FMT_RESIDUAL, rq.RQ_FMT_BF16])
+def test_a_prompt_then_tokens_then_the_cache_read_back(fmt):
+    """The operators as a serving loop uses them: a prompt in chunks (append, then the chunk's attention at every loop),
+    then single tokens, all with one window and sinks; what is read back in the end is what the attention saw."""
+    Lg, B, Hk, Hq, window, sinks = (4 if fmt == rq.RQ_FMT_RESIDUAL else 1), 2, 2, 4, 150, 6
+    cfg = rq.make_config(num_layers=1, num_loops=Lg, loops_per_group=Lg, batch=B, max_tokens=512, max_tail_tokens=200,
+                         num_kv_heads=Hk, num_q_heads=Hq, format=fmt)
+    cache = H.guarded_cache(cfg)
+    K, V = synth.group_kv(7, 0, 0, Lg, (0.1, 0.2, 0.3)[:max(Lg - 1, 1)], B, 400, Hk, device="cuda")
+    done = 0
+    for n in (130, 200, 1, 33, 1, 1):
+        for j in range(Lg):
+            cache.append(0, j, K[j][:, done:done + n].contiguous(), V[j][:, done:done + n].contiguous())
+            q = queries(100 * done + j, B, n, Hq, 128)
+            if n > 1:
+                got = cache.prefill_window(0, j, q, window, sinks)
+            else:
+                got = cache.decode_window(0, j, q[:, 0].contiguous(), window, sinks)[:, None]
+            k, v = (x.double().cpu().numpy().transpose(0, 2, 1, 3) for x in cache.read(0, j, dtype=torch.float32))
+            assert k.shape[2] == done + n
+            if j < Lg - 1:
+                assert np.array_equal(k[:, :, done:], K[j][:, done:done + n].double().cpu().numpy().transpose(0, 2, 1, 3))
+            check(got, reference([np.stack([k[b], v[b]]) for b in range(B)], q, window, sinks), 1e-3, 2e-3)
+        done += n
+    cache.check()
+    cache.close()
