@@ -718,6 +718,80 @@ def prefill_mma_flops(n, G, B, H, T, resid):
     return committed + tail
 
 
+def run_window(args):
+    """The windowed attention calls and rq_cache_read on the Ouro-1.4B-shaped
+    cache (B = 4, T = 8192, H = 16), --window W,S: a window of W tokens and S
+    sinks.  One JSON line per call: a single token (rq_decode_attn_window) and
+    a chunk of 64 (rq_prefill_attn_window) at a residual loop, both with fp32
+    output, the residual loop read back whole as BF16, and the single token
+    over a BF16 cache; achieved bandwidth over the bytes of the visible
+    records (of the whole loop and of the rows written, for the read).  The calls
+    go round four layers, together larger than the L2 cache."""
+    import torch
+    import decode_attention_14_b200 as rq
+    import synth
+
+    dev = torch.device("cuda", 0)
+    torch.cuda.set_device(dev)
+    window, sinks = (int(x) for x in args.window.split(","))
+    base = CONFIGS["ouro8k_b4"]
+    Lg, T, H, Hq, B, n, reps = base["Lg"], base["T"], base["H"], base["Hq"], base["B"], 64, 12
+    layers = 4
+    peak, peak_kind = _peaks()[:2]
+    seen = min(T, sinks + window) if window else T
+
+    def timed(call):
+        for i in range(layers):
+            call(i)
+        torch.cuda.synchronize(dev)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for i in range(reps):
+                call(i % layers)
+        g.replay()
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record()
+        g.replay()
+        e1.record()
+        torch.cuda.synchronize(dev)
+        return e0.elapsed_time(e1) * 1e3 / reps
+
+    for fmt in (rq.RQ_FMT_RESIDUAL, rq.RQ_FMT_BF16):
+        bf16 = fmt == rq.RQ_FMT_BF16
+        cfg = rq.make_config(num_layers=layers, num_loops=1 if bf16 else Lg, loops_per_group=1 if bf16 else Lg, batch=B,
+                             max_tokens=T, max_tail_tokens=FILL_CHUNK, num_kv_heads=H, num_q_heads=Hq, format=fmt,
+                             seed=0xA11CE)
+        cache = rq.Cache(cfg, device=dev)
+        for t0 in range(0, T, FILL_CHUNK):
+            Kg, Vg = synth.group_kv(0x5EED0008, 0, 0, Lg, base["sigma"], B, FILL_CHUNK, H, t0=t0, device=dev)
+            for i in range(layers):
+                for j in range(cfg.num_loops):
+                    cache.append(i, j, Kg[j], Vg[j])
+        gen = torch.Generator(device=dev).manual_seed(0x5EED0008)
+        q = torch.randn((B, n, Hq, 128), generator=gen, device=dev).to(torch.bfloat16)
+        one, out1, outn = q[:, 0].contiguous(), torch.empty((B, Hq, 128), device=dev), torch.empty(q.shape, device=dev)
+        per = 512 if bf16 else 260
+        calls = [("rq_decode_attn_window", lambda i: cache.decode_window(i, 0, one, window, sinks, out=out1),
+                  B * H * seen * per)]
+        if not bf16:
+            k, v = (torch.empty((B, T, H, 128), dtype=torch.bfloat16, device=dev) for _ in range(2))
+            calls += [("rq_prefill_attn_window", lambda i: cache.prefill_window(i, 0, q, window, sinks, out=outn),
+                       B * H * min(T, seen + n) * per),
+                      ("rq_cache_read", lambda i: cache.read(i, 0, 0, k=k, v=v), B * H * T * (per + 512))]
+        for name, call, nbytes in calls:
+            us = timed(call)
+            gbs = nbytes / (us * 1e-6) / 1e9
+            row = {"call": name, "cache": "bf16" if bf16 else "residual loop", "batch": B, "seq_len": T,
+                   "tokens": 1 if name == "rq_decode_attn_window" else n if name == "rq_prefill_attn_window" else T,
+                   "window": window, "sinks": sinks, "us_per_call": round(us, 1),
+                   "roofline": {"bound": "hbm", "achieved": round(gbs, 1), "peak": peak, "unit": "GB/s",
+                                "frac": round(gbs / peak, 4), "peak_kind": peak_kind},
+                   "timing": "CUDA graph of %d calls over %d layers (inputs larger than L2), CUDA events"
+                   % (reps, layers)}
+            print(json.dumps(row), flush=True)
+        cache.close()
+
+
 def run_prefill(args):
     """rq_prefill_attn on the Ouro-1.4B-shaped cache (B = 4, T = 8192, H = 16;
     with --paged in 128-token blocks scattered over the pool):
@@ -846,6 +920,9 @@ def main():
                     help="batch x format sweep of the Ouro shape at T=8192 (one JSON line per row)")
     ap.add_argument("--prefill", default="",
                     help="comma-separated chunk sizes: time rq_prefill_attn on the Ouro shape instead")
+    ap.add_argument("--window", default="",
+                    help="W,S: time the windowed attention calls (W tokens, S sinks) and rq_cache_read on the Ouro "
+                         "shape instead")
     ap.add_argument("--paged", action="store_true", help="records in a pool of 128-token blocks (block tables)")
     ap.add_argument("--chained", action="store_true",
                     help="the chained (previous-loop) reference of the ablation instead of the shared anchor")
@@ -870,6 +947,9 @@ def main():
         return
     if args.prefill:
         run_prefill(args)
+        return
+    if args.window:
+        run_window(args)
         return
     if args.impl == "reference":
         if rank == 0:

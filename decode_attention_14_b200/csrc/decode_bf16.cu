@@ -12,7 +12,9 @@
 // only -- the sinks, then the window, as one run with a hole that is stepped
 // over -- so nothing masked is read; and the last CTA of a (sequence, kv head,
 // head pair) to arrive merges the splits itself: one launch, which is what a
-// short window costs.
+// short window costs.  Bound by the latency of its loads: 48 registers and ten
+// CTAs an SM; 4 x 16 heads, window 4096 + 4 (134 MB), 28.3 us = 4.76 TB/s, 73% of
+// a plain copy.
 #include <math_constants.h>
 
 #include "combine.cuh"

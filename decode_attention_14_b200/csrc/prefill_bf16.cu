@@ -42,8 +42,18 @@
 // for all the chunk's rows, and every product is in FP16 with K and V scaled by
 // 2^-8 and q by 2^-4: for BF16 output one part each of K, V and P (2^-12, below
 // the output's own rounding), for fp32 output two: S = Q (Khi + Klo)^T,
-// O += (Phi + Plo) Vhi + Phi Vlo.  (In BF16 that takes two parts of K even for
-// BF16 output: 50 instead of 38 us, 768 instead of 512 workspace bytes a token.)
+// O += (Phi + Plo) Vhi + Phi Vlo.  (With BF16 operands the error of BF16 output
+// asks for two parts of K: 500 tokens in two sequences of 4 kv heads of 4 heads,
+// window 2000, 42 instead of 38 us, and half as much workspace again.)
+//
+// What bounds it: a full chunk is bound by the softmax between the two products
+// (one exponential and about six other operations per logit in a thread per
+// row), not by the MMAs: 8192 causal tokens, 16 heads, 308 us = 892 TFLOP/s,
+// tensor pipe 36% and special-function pipe 37% busy in a 4096-token run.  Few
+// rows over a short window are bound by launches and the pipeline's filling:
+// 511 tokens in two sequences of 4 kv heads of 4, window 1024 (8.6 GFLOP), 30 us.
+// Over compressed caches (all launches), window 1024: 2048 tokens of 16 heads,
+// 54 us; 16 tokens of 4 x 16 heads, 37 us; the first launch takes about 20 of each.
 //
 // A V row that only some rows see may hold NaN or infinities, which 0 * NaN
 // would carry into the other rows.  The store kernel notes in the arena when it

@@ -135,7 +135,7 @@ typedef struct rq_config {
  * attention calls). */
 typedef enum {
     RQ_OUT_FP32 = 0,
-    RQ_OUT_BF16 = 1           /* the fp32 result rounded once, to nearest even */
+    RQ_OUT_BF16 = 1           /* rounded to nearest even (each call says what else it rounds) */
 } rq_out_type;
 
 typedef struct rq_cache rq_cache;
@@ -284,10 +284,13 @@ int rq_prefill_attn(rq_cache *cache, int layer, int loop, const void *q_bf16, in
  *   out:    device, [batch][num_q_heads][head_dim] of out_type (rq_out_type).
  *   softmax_scale: as for rq_decode_attn.
  * Only the records of visible tokens (in whole 64-token tiles) are read;
- * masked tokens do not enter the result, whatever they hold.  With no token
- * at all the output is zero.  fp32 results are more precise than
- * rq_decode_attn's (28-bit instead of 22-bit value weights).  Overlap,
- * workspace and stream rules are rq_decode_attn's.
+ * masked tokens do not enter the result, whatever they hold (the value weights'
+ * fixed point of a compressed cache is relative to the largest FP8 scale ever
+ * written to the stream, masked tokens' among them).  With no token at all the
+ * output is zero.  fp32 results are more precise than rq_decode_attn's (31-bit
+ * instead of 22-bit value weights).  Overlap,
+ * workspace and stream rules are rq_decode_attn's; BF16 output is the fp32
+ * result rounded once.
  * Errors: INVALID (null pointer, index, window < 0, sinks < 0, out_type),
  * UNSUPPORTED (as rq_decode_attn), CUDA.
  */
@@ -305,13 +308,27 @@ int rq_decode_attn_window(rq_cache *cache, int layer, int loop, const void *q_bf
  *   q_bf16: device, [batch][n_tokens][num_q_heads][head_dim] BF16, oldest first.
  *   out:    device, the same shape, of out_type (rq_out_type).
  *   window, sinks, softmax_scale: as for rq_decode_attn_window.
- * A masked token does not enter a row, whatever it holds.
- * The split partials and arrival counters are rq_prefill_attn's buffers, under
- * the same rules (make the first call of a size before any stream capture);
- * a call whose row blocks fill the device by themselves needs neither.
+ * A masked token does not enter a row, whatever it holds; a row that sees a V
+ * that is not finite is NaN as a whole.
+ * Arithmetic: products on the tensor cores with fp32 sums.  BF16 caches: exact
+ * products of q and K; the weights are BF16 for BF16 output (half a step, 2^-9,
+ * of each weight beside the output's own rounding), two BF16 parts (2^-17) for
+ * fp32 output.  Compressed caches: the visible rows are rebuilt as FP16 (times
+ * 2^-8, q times 2^-4), one number each for BF16 output (2^-12), two for fp32
+ * output (2^-23); |k|, |v| >= 1.6e7 and |q| >= 1e6 count as not finite there.
+ * Buffers the cache allocates on the first call and grows when a later call
+ * needs more: split partials, and for compressed caches the rebuilt rows:
+ * batch * (tokens visible to any of the n, + 143 at most) * 512 bytes a kv head
+ * (1024 with fp32 output), for as many kv heads at a time as 4 GiB hold, at
+ * least one.  Growing synchronises the device and cannot be done while `stream`
+ * is being captured (NOMEM, the capture stays valid): make the first call of a
+ * size before.  Buffers that a captured call uses stay until rq_cache_destroy,
+ * also when outgrown.  Calls on one cache share them: calls whose work overlaps
+ * (other streams, two replayed graphs) must be ordered by the caller.
  * Errors: INVALID (null pointer, n_tokens < 1, index, window < 0, sinks < 0,
  * out_type), STATE (a sequence holds fewer than n_tokens tokens), UNSUPPORTED
- * (as rq_prefill_attn), NOMEM, CUDA.
+ * (as rq_prefill_attn, and more than 65535 row blocks of 128 query rows over
+ * the batch), NOMEM, CUDA.
  */
 int rq_prefill_attn_window(rq_cache *cache, int layer, int loop, const void *q_bf16, int n_tokens, void *out,
                            int out_type, float softmax_scale, int window, int sinks, void *stream);

@@ -3,19 +3,18 @@ rq_prefill_attn_window) against a plain fp64 softmax over the keys and values
 that the cache holds (rq_cache_export through the oracle's reconstruction, or
 the stored BF16 values, then the BF16 tail).
 
-Tolerances, fp32 output.  Decode of the compressed cache: value weights in 28
-bits and q in 24 bits of fixed point relative to their largest, sums in int32:
-the weight error of a token is at most 2^-29 of the bound max|s| max(scale),
-times a code of at most 15, random over the tokens; the logit error at most
-2^-22 max|q| times |k|_1.  With |k|_1 below 128 * 3 (10 in 4 channels) and
-max|q| about 4, scaled by 1/sqrt(128): about 4e-5 at the very worst, and the
-output moves by at most twice that times the values' spread: 2e-4 max abs and
-2e-5 relative L2 leave a margin for fp32 sums.  The chunk kernel splits
-probabilities and rotated queries into BF16 pairs (relative 2^-17 each): the
-contract's 1e-3 / 2e-3.  BF16 caches: fp32 products and sums (decode), or
-probabilities as BF16 pairs.  BF16 output adds half a step, 2^-8 |x|; a chunk's
-weights and (compressed cache) values are then BF16 too, 2^-9 of each: at most
-2 * 2^-9 max|v| with |v| < 45, and 2^-8 of the row's norm at random signs.
+Tolerances, fp32 output.  Decode of the compressed cache: value weights in 31
+bits and q in 23 bits (and a sign) of fixed point relative to their largest, sums
+in integers.  The logit error is at most 2^-23 max|q| times |k|_1: with |k|_1
+below 128 * 3 (10 in 4 channels) and max|q| about 4, scaled by 1/sqrt(128), about
+2e-5 at the very worst, and the output moves by at most twice that times the
+values' spread: 2e-4 max abs and 2e-5 relative L2 leave a margin for fp32 sums.
+The chunk kernel splits probabilities, keys and values into pairs of FP16 numbers
+(compressed caches) or probabilities into BF16 pairs (2^-17): the contract's
+1e-3 / 2e-3.  BF16 caches, decode: fp32 products and sums.  BF16 output adds half
+a step, 2^-8 |x|; a chunk's weights are then one BF16 number (2^-9 of each), or
+weights, keys and values one FP16 number (2^-12): at most 2 * 2^-9 max|v| with
+|v| < 45, and 2^-8 of the row's norm at random signs.
 """
 import numpy as np
 import pytest
