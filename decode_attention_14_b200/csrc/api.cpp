@@ -695,14 +695,16 @@ int rq_append(rq_cache *c, int layer, int loop, const void *k, const void *v, in
 // (stride = the split count this call uses).
 // app_k != nullptr: append app_n tokens to the loop first (rq_append_decode_attn).
 // win != nullptr: a windowed call (`out` then points to elements of win->out_type).
+// Its query is row `row` of `rows` per sequence in q and out, and the rows
+// behind it are newer tokens, which it does not see.
 struct WindowSpec {
-    int window, sinks, out_type;
+    int window, sinks, out_type, rows, row;
 };
 // The arguments of the windowed calls as the caller gave them; window 0
 // (every token visible) becomes a window no sequence reaches.
 static bool window_spec(int window, int sinks, int out_type, WindowSpec *w) {
     if (window < 0 || sinks < 0 || (out_type != RQ_OUT_FP32 && out_type != RQ_OUT_BF16)) return false;
-    *w = WindowSpec{window > 0 ? window : INT_MAX, window > 0 ? sinks : 0, out_type};
+    *w = WindowSpec{window > 0 ? window : INT_MAX, window > 0 ? sinks : 0, out_type, 1, 0};
     return true;
 }
 static int decode_common(rq_cache *c, int layer, int loop, const void *q, float *out, float scale,
@@ -779,10 +781,18 @@ static int decode_common(rq_cache *c, int layer, int loop, const void *q, float 
     if (win) {
         a.window = win->window;
         a.sinks = win->sinks;
+        const size_t first = (size_t)win->row * a.Hq * kHeadDim;
+        a.ldq = win->rows * a.Hq;
+        a.q += first;
+        a.out += first;
         if (win->out_type == RQ_OUT_BF16) {
-            a.out16 = (uint16_t *)out;
+            a.out16 = (uint16_t *)out + first;
             a.out = nullptr;
         }
+        const int newer = win->rows - 1 - win->row, old = std::max(0, newer - a.n_tail);
+        a.n_tail = std::max(0, a.n_tail - newer);
+        a.T -= old;
+        for (int b = 0; b < a.B; b++) a.seqT.v[b] -= old;
         if (bf16) {   // the visible tokens are one run there
             int run = 0;
             for (int b = 0; b < a.B; b++) {
@@ -840,6 +850,7 @@ static int decode_common(rq_cache *c, int layer, int loop, const void *q, float 
     cb.q = a.q;
     cb.out = a.out;
     cb.out16 = a.out16;
+    cb.ldq = win ? a.ldq : a.Hq;
     cb.window = a.window;
     cb.sinks = a.sinks;
     cb.tail_k = a.tail_k;
@@ -887,13 +898,6 @@ int rq_decode_attn_bf16(rq_cache *c, int layer, int loop, const void *q, float *
     return decode_common(c, layer, loop, q, out, scale, stream, true);
 }
 
-int rq_decode_attn_window(rq_cache *c, int layer, int loop, const void *q, void *out, int out_type, float scale,
-                          int window, int sinks, void *stream) {
-    WindowSpec w;
-    if (!c || !window_spec(window, sinks, out_type, &w)) return RQ_ERR_INVALID;
-    return decode_common(c, layer, loop, q, (float *)out, scale, stream, c->lay.cfg.format == RQ_FMT_BF16, nullptr, 0,
-                         nullptr, 0, nullptr, nullptr, 0, &w);
-}
 
 }  // extern "C"
 
@@ -1007,6 +1011,32 @@ int plan_rebuild(rq_cache *c, const PrefillArgs &a, cudaStream_t st, ReadArgs *r
     return RQ_OK;
 }
 
+// New tokens up to which a windowed chunk runs token by token through the decode
+// kernels, which read the visible records once for every token and every two
+// heads (`passes`), instead of rebuilding them for the tensor cores once for all.
+// Compressed caches, one residual, BF16 output, 4 x 16 heads, us for 1 / 2 / 3 / 4
+// tokens: 8192 visible tokens 38 / 77 / 115 / 153 against 174, 1024: 11 / 24 / 37 /
+// 50 against 36, 128: 8 / 17 / 25 / 33 against 14 / 18 / 18 / 18; heads in groups
+// of 4, 8 kv heads, 8192: 24 against 31, 1024: 13.6 against 13.1; groups of 8, 4 kv
+// heads, 16384: 38 against 33.  fp32 output leaves more room (250 / 53 / 17, 40 /
+// 15.2, 43).  BF16 caches: one token, 4 x 16 heads, 1024 visible, 12.2 against
+// 16.4, 128: 7.0 against 8.5, 8192: 49 against 47; groups of 4 (one pass over K and V
+// for the four on the tensor cores, two in the decode kernel), 8 kv heads, 8192: 28
+// against 13, 128: 8.1 against 8.2; groups of 8, 4 kv heads, 16384: 37 against 15 --
+// so there rq_decode_attn_window goes to the chunk's kernel too (fp32 output: error
+// 1 to 3e-6 relative, BF16 pairs of weights, instead of 4e-7, for half the time).
+int few_rows(const rq_cache *c, const SeqLens &lens, int n_tail, const WindowSpec &win) {
+    const rq_config &cfg = c->lay.cfg;
+    const int G = cfg.num_q_heads / cfg.num_kv_heads, passes = G > 2 ? G / 2 : 1;
+    if (cfg.format == RQ_FMT_BF16) return passes == 1 ? 1 : 0;
+    long long seen = 0;
+    for (int b = 0; b < cfg.batch; b++)
+        seen += std::min((long long)lens.v[b] + n_tail, (long long)win.window + win.sinks);
+    seen *= cfg.num_kv_heads;
+    const int most = seen >= 1 << 18 ? 4 : seen >= 1 << 16 ? 2 : 1;
+    return std::max(passes <= 2 ? 1 : 0, most / passes);
+}
+
 // win == nullptr: rq_prefill_attn
 int prefill_common(rq_cache *c, int layer, int loop, const void *q, int n, void *out, float scale, void *stream,
                    const WindowSpec *win) {
@@ -1045,6 +1075,16 @@ int prefill_common(rq_cache *c, int layer, int loop, const void *q, int n, void 
     // the n new tokens must be the most recent of every sequence
     for (int b = 0; b < cfg.batch; b++)
         if (a.seqT.v[b] + a.n_tail < n) return RQ_ERR_STATE;
+    if (win && n <= few_rows(c, a.seqT, a.n_tail, *win)) {
+        WindowSpec w = *win;
+        w.rows = n;
+        for (w.row = 0; w.row < n; w.row++) {
+            const int s = decode_common(c, layer, loop, q, (float *)out, scale, stream, bf16, nullptr, 0, nullptr, 0, nullptr,
+                                        nullptr, 0, &w);
+            if (s != RQ_OK) return s;
+        }
+        return RQ_OK;
+    }
     a.q = (const uint16_t *)q;
     a.out = (float *)out;
     a.B = cfg.batch;
@@ -1082,9 +1122,14 @@ int prefill_common(rq_cache *c, int layer, int loop, const void *q, int n, void 
         a.counters = a.S > 0 ? c->prefill_cnt : nullptr;
         return cuda_status(launch_prefill(a, cfg.anchor_bits, cfg.resid_bits, st));
     }
-    int s = prefill_workspace(c, a.S > 1 ? partials : 0, 0, st);   // one split writes its rows directly
-    if (s != RQ_OK) return s;
-    a.partials = c->prefill_ws;
+    int s = RQ_OK;   // one split writes its rows directly
+    if (a.S > 1 && n == 1 && a.S <= L.splits_max) {   // a token's partials fit the arena's workspace
+        a.partials = (float *)(c->base + L.off_partials);
+    } else {
+        s = prefill_workspace(c, a.S > 1 ? partials : 0, 0, st);
+        if (s != RQ_OK) return s;
+        a.partials = c->prefill_ws;
+    }
     if (bf16) {
         s = cuda_status(launch_prefill_bf16(a, bf16_ptr(c, layer, loop, 0), bf16_ptr(c, layer, loop, 1), nonfinite_ptr(c),
                                             st));
@@ -1104,6 +1149,24 @@ int prefill_common(rq_cache *c, int layer, int loop, const void *q, int n, void 
 }  // namespace
 
 extern "C" {
+
+int rq_decode_attn_window(rq_cache *c, int layer, int loop, const void *q, void *out, int out_type, float scale,
+                          int window, int sinks, void *stream) {
+    WindowSpec w;
+    if (!c || !window_spec(window, sinks, out_type, &w)) return RQ_ERR_INVALID;
+    const rq_config &cfg = c->lay.cfg;
+    const bool bf16 = cfg.format == RQ_FMT_BF16;
+    // heads in groups of four and more over a BF16 cache: the chunk's kernel, which reads K and V once for
+    // the group (see few_rows); it has no sequence without tokens
+    if (bf16 && cfg.num_q_heads >= 4 * cfg.num_kv_heads && layer >= 0 && layer < cfg.num_layers && loop >= 0 &&
+        loop < cfg.num_loops) {
+        const int *len = seq_lens(c, (size_t)layer * cfg.num_loops + loop);
+        if (*std::min_element(len, len + cfg.batch) > 0)
+            return prefill_common(c, layer, loop, q, 1, out, scale, stream, &w);
+    }
+    return decode_common(c, layer, loop, q, (float *)out, scale, stream, bf16, nullptr, 0, nullptr, 0, nullptr, nullptr, 0,
+                         &w);
+}
 
 int rq_prefill_attn(rq_cache *c, int layer, int loop, const void *q, int n, float *out, float scale, void *stream) {
     return prefill_common(c, layer, loop, q, n, out, scale, stream, nullptr);

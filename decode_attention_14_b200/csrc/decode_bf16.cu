@@ -12,7 +12,7 @@
 // only -- the sinks, then the window, as one run with a hole that is stepped
 // over -- so nothing masked is read; and the last CTA of a (sequence, kv head,
 // head pair) to arrive merges the splits itself: one launch, which is what a
-// short window costs.  Bound by the latency of its loads: 48 registers and ten
+// short window costs (groups of four heads and more go to prefill_bf16.cu).  Bound by the latency of its loads: 48 registers and ten
 // CTAs an SM; 4 x 16 heads, window 4096 + 4 (134 MB), 28.3 us = 4.76 TB/s, 73% of
 // a plain copy.
 #include <math_constants.h>
@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(128, WIN ? (GK == 1 ? 10 : 7) : 0) decode_bf16
 
 #pragma unroll
     for (int gq = 0; gq < GK; gq++)
-        s_q[gq][tid] = bf16_to_f32(a.q[((size_t)b * a.Hq + hq0 + gq) * kHeadDim + tid]) * a.scale_log2;
+        s_q[gq][tid] = bf16_to_f32(a.q[((size_t)b * (WIN ? a.ldq : a.Hq) + hq0 + gq) * kHeadDim + tid]) * a.scale_log2;
     __syncthreads();
     float qa[GK][16];
 #pragma unroll
@@ -173,9 +173,10 @@ __global__ void __launch_bounds__(128, WIN ? (GK == 1 ? 10 : 7) : 0) decode_bf16
         for (int gq = 0; gq < GK; gq++) {
             const size_t row = (size_t)b * a.Hq + hq0 + gq;
             // 8 splits a batch: 16 would cost the registers of two CTAs an SM
-            combine_row<8>(a.partials + row * a.splits_max * kPartialStride, a.S, a.q + row * kHeadDim, a.scale_log2,
-                        nullptr, nullptr, 0, 0, a.out16 ? nullptr : a.out + row * kHeadDim, tid, &s_red[0][0],
-                        BlockSync(), TailMask{0, 0}, a.out16 ? a.out16 + row * kHeadDim : nullptr);
+            const size_t io = (size_t)b * a.ldq + hq0 + gq;
+            combine_row<8>(a.partials + row * a.splits_max * kPartialStride, a.S, a.q + io * kHeadDim, a.scale_log2,
+                        nullptr, nullptr, 0, 0, a.out16 ? nullptr : a.out + io * kHeadDim, tid, &s_red[0][0],
+                        BlockSync(), TailMask{0, 0}, a.out16 ? a.out16 + io * kHeadDim : nullptr);
         }
     }
 }
@@ -186,13 +187,13 @@ __global__ void __launch_bounds__(128) combine_kernel(const CombineArgs a) {
     __shared__ float s_red[4];
     const int hq = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
     const int h = hq / a.G;
-    const size_t row = (size_t)b * a.Hq + hq;
+    const size_t row = (size_t)b * a.Hq + hq, io = (size_t)b * a.ldq + hq;
     const size_t trow = ((size_t)b * a.tail_cap * a.H + h) * kHeadDim;
-    combine_row(a.partials + row * a.splits_max * kPartialStride, a.S, a.q + row * kHeadDim, a.scale_log2,
+    combine_row(a.partials + row * a.splits_max * kPartialStride, a.S, a.q + io * kHeadDim, a.scale_log2,
                 a.tail_k ? a.tail_k + trow : nullptr, a.tail_v ? a.tail_v + trow : nullptr, (size_t)a.H * kHeadDim,
-                a.n_tail, a.out16 ? nullptr : a.out + row * kHeadDim, tid, s_red, BlockSync(),
+                a.n_tail, a.out16 ? nullptr : a.out + io * kHeadDim, tid, s_red, BlockSync(),
                 a.window > 0 ? tail_mask(0, a.n_tail, a.window, a.sinks) : TailMask{0, 0},
-                a.out16 ? a.out16 + row * kHeadDim : nullptr);
+                a.out16 ? a.out16 + io * kHeadDim : nullptr);
 }
 
 }  // namespace

@@ -625,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, GK == 1 ? RQ_DECODE_MIN_CTAS : 3) de
 
     // q (log2-domain scale folded in) and R q, then 24-bit fixed-point planes
     for (int gq = 0; gq < GK; gq++)
-        s_q[gq][0][tid] = bf16_to_f32(a.q[((size_t)b * a.Hq + hq0 + gq) * kHeadDim + tid]) * a.scale_log2;
+        s_q[gq][0][tid] = bf16_to_f32(a.q[((size_t)b * (WIN ? a.ldq : a.Hq) + hq0 + gq) * kHeadDim + tid]) * a.scale_log2;
     consumer_sync();
     if (RESID && warp < GK) {
         const int gq = warp;
@@ -1041,15 +1041,17 @@ __global__ void __launch_bounds__(kThreads, GK == 1 ? RQ_DECODE_MIN_CTAS : 3) de
             const size_t row = (size_t)b * a.Hq + hq0 + gq;
             const size_t trow = ((size_t)b * a.tail_cap * a.H + h) * kHeadDim;
             const auto tail_k = a.tail_k ? a.tail_k + trow : nullptr, tail_v = a.tail_v ? a.tail_v + trow : nullptr;
-            if (WIN)
-                combine_row(a.partials + row * a.splits_max * kPartialStride, a.S, a.q + row * kHeadDim, a.scale_log2,
+            if (WIN) {
+                const size_t io = (size_t)b * a.ldq + hq0 + gq;
+                combine_row(a.partials + row * a.splits_max * kPartialStride, a.S, a.q + io * kHeadDim, a.scale_log2,
                             tail_k, tail_v, (size_t)a.H * kHeadDim, a.n_tail,
-                            a.out16 ? nullptr : a.out + row * kHeadDim, tid, &s_red[0][0], ConsumerSync(),
-                            tail_mask(a.seqT.v[b], a.n_tail, a.window, a.sinks), a.out16 ? a.out16 + row * kHeadDim : nullptr);
-            else
+                            a.out16 ? nullptr : a.out + io * kHeadDim, tid, &s_red[0][0], ConsumerSync(),
+                            tail_mask(a.seqT.v[b], a.n_tail, a.window, a.sinks), a.out16 ? a.out16 + io * kHeadDim : nullptr);
+            } else {
                 combine_row(a.partials + row * a.splits_max * kPartialStride, a.S, a.q + row * kHeadDim, a.scale_log2,
                             tail_k, tail_v, (size_t)a.H * kHeadDim, a.n_tail, a.out + row * kHeadDim, tid, &s_red[0][0],
                             ConsumerSync());
+            }
         }
     }
 }

@@ -195,6 +195,7 @@ struct DecodeArgs {
     // output in BF16 instead of `out`
     int window, sinks, s_sink;
     uint16_t *out16;
+    int ldq;                  // windowed calls: rows of q and out between two sequences (Hq, or a chunk's n Hq)
 };
 
 // Tokens [*t0, *t0 + *n) of split `split` of S: the ceil(T/64) tiles are
@@ -256,6 +257,7 @@ struct CombineArgs {
     float scale_log2;
     int window, sinks;        // a windowed call's (window 0: none); every sequence then holds no committed token
     uint16_t *out16;          // the output in BF16 instead of `out`, or null
+    int ldq;                  // rows of q and out between two sequences
 };
 
 // Block-table writes and whole-block copies of a paged cache (copy-on-write

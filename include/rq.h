@@ -288,9 +288,11 @@ int rq_prefill_attn(rq_cache *cache, int layer, int loop, const void *q_bf16, in
  * fixed point of a compressed cache is relative to the largest FP8 scale ever
  * written to the stream, masked tokens' among them).  With no token at all the
  * output is zero.  fp32 results are more precise than rq_decode_attn's (31-bit
- * instead of 22-bit value weights).  Overlap,
- * workspace and stream rules are rq_decode_attn's; BF16 output is the fp32
- * result rounded once.
+ * instead of 22-bit value weights); BF16 output is the fp32 result rounded once.
+ * RQ_FMT_BF16 with four or more query heads a kv head (and no empty sequence):
+ * the arithmetic of rq_prefill_attn_window over such a cache, on the tensor
+ * cores.  No buffer beyond the arena is used.  Overlap, workspace and stream
+ * rules are rq_decode_attn's.
  * Errors: INVALID (null pointer, index, window < 0, sinks < 0, out_type),
  * UNSUPPORTED (as rq_decode_attn), CUDA.
  */
@@ -309,8 +311,10 @@ int rq_decode_attn_window(rq_cache *cache, int layer, int loop, const void *q_bf
  *   out:    device, the same shape, of out_type (rq_out_type).
  *   window, sinks, softmax_scale: as for rq_decode_attn_window.
  * A masked token does not enter a row, whatever it holds; a row that sees a V
- * that is not finite is NaN as a whole.
- * Arithmetic: products on the tensor cores with fp32 sums.  BF16 caches: exact
+ * that is not finite is not finite either (from the tensor cores NaN as a whole).
+ * Arithmetic: one to four tokens, where that is less work, run one by one as
+ * rq_decode_attn_window does (n_tokens, the heads per kv head and the number of
+ * visible tokens decide).  Else: products on the tensor cores with fp32 sums.  BF16 caches: exact
  * products of q and K; the weights are BF16 for BF16 output (half a step, 2^-9,
  * of each weight beside the output's own rounding), two BF16 parts (2^-17) for
  * fp32 output.  Compressed caches: the visible rows are rebuilt as FP16 (times

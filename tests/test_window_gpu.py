@@ -561,7 +561,7 @@ def test_bf16_prefill_repeats_itself():
 
 def test_prefill_window_beyond_one_workspace():
     """More rebuilt rows than the workspace holds at once (4 GiB): the kv heads go in groups.  8 sequences of 160 000
-    tokens at an anchor loop; the last token's row against the single-token call, for every head."""
+    tokens at an anchor loop; the last of five tokens' rows against the single-token call, for every head."""
     B, Hk, T = 8, 4, 160000
     cfg = rq.make_config(num_layers=1, num_loops=1, loops_per_group=1, batch=B, max_tokens=T, max_tail_tokens=0,
                          num_kv_heads=Hk, num_q_heads=Hk)
@@ -570,7 +570,7 @@ def test_prefill_window_beyond_one_workspace():
     for t in range(0, T, 20000):
         k, v = (torch.randn((B, 20000, Hk, 128), generator=g, device="cuda").bfloat16() for _ in range(2))
         cache.append(0, 0, k, v)
-    q = queries(17, B, 3, Hk, 128)
+    q = queries(17, B, 5, Hk, 128)
     got = cache.prefill_window(0, 0, q, 0)
     ref = cache.decode_window(0, 0, q[:, -1].contiguous(), 0).double().cpu().numpy()
     for h in range(Hk):
@@ -578,6 +578,54 @@ def test_prefill_window_beyond_one_workspace():
         assert np.linalg.norm(g_h - r_h) <= 1e-3 * np.linalg.norm(r_h) and np.abs(g_h - r_h).max() <= 2e-3, h
     cache.check()
     cache.close()
+
+
+@pytest.mark.parametrize("Hq,paged", [(64, False), (32, True)])
+def test_a_few_tokens_over_many(Hq, paged):
+    """Chunks short enough to run token by token: committed, in the tail, and partly in each; one longer."""
+    kw = dict(block_tokens=128, num_blocks=70, prepare=lambda c: c.shuffle_free_blocks(3)) if paged else {}
+    bt = H.build(loops=2, Lg=2, B=2, T=4200, H=32, Hq=Hq, seed=0x5EEDEE04, **kw)
+    lens = [4200, 4137]
+    bt.cache.truncate_seq(0, 0, 1, lens[1])
+    K, V = bt.inputs[(0, 0)]
+    tail = torch.randn((2, 2, 2, 32, 128), device="cuda", generator=torch.Generator("cuda").manual_seed(1)).bfloat16()
+    bt.cache.append(0, 0, tail[0].contiguous(), tail[1].contiguous())
+    bt.inputs[(0, 0)] = tuple([torch.cat((X[j], tail[i]), 1) for j in range(2)] for i, X in ((0, K), (1, V)))
+    bt.n_tail = 2
+    for loop in (0, 1):
+        kv = keys_values(bt, 0, loop, lens)
+        for n in (1, 2, 3, 4, 5):
+            q = queries(20 + n, 2, n, Hq, 128)
+            for window, sinks, dtype in ((0, 0, torch.float32), (4150, 4, torch.bfloat16), (1100, 30, torch.float32)):
+                few = n <= (4 if window != 1100 else 2)
+                tol = (2e-5, 2e-4) if few else (1e-3, 2e-3) if dtype == torch.float32 else (2.0 ** -8, 0.18)
+                check(bt.cache.prefill_window(0, loop, q, window, sinks, dtype=dtype), reference(kv, q, window, sinks), *tol)
+    bt.cache.check()
+    bt.cache.close()
+
+
+@pytest.mark.parametrize("Hq", [8, 16])
+def test_decode_of_grouped_heads_over_a_bf16_cache(Hq):
+    """One pass over K and V for 4 or 8 heads (no sequence is empty); tolerances as for a chunk over such a cache.  Captured
+    as the cache's first call too, and with an empty sequence, the same rows to the two paths' tolerances."""
+    bt, lens = _bf16(1300, B=3, Hq=Hq, lens=[1300, 77, 1])
+    q = queries(26, 3, Hq, 128)
+    out, g = torch.zeros((3, Hq, 128), device="cuda"), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        bt.cache.decode_window(0, 0, q, 700, 4, out=out)
+    kv = keys_values(bt, 0, 0, lens)
+    for window, sinks in WINDOWS + [(1234, 64), (700, 600)]:
+        ref = reference(kv, q[:, None], window, sinks)[:, 0]
+        check(bt.cache.decode_window(0, 0, q, window, sinks), ref, 1e-5, 2e-4)
+        check(bt.cache.decode_window(0, 0, q, window, sinks, dtype=torch.bfloat16), ref, 2.0 ** -9, 9e-2)
+    g.replay()
+    assert torch.equal(out, bt.cache.decode_window(0, 0, q, 700, 4))
+    bt.cache.truncate_seq(0, 0, 2, 0)
+    with_empty = bt.cache.decode_window(0, 0, q, 700, 4)
+    assert (with_empty[2] == 0).all()
+    check(with_empty[:2], out[:2].double().cpu().numpy(), 1.4e-5, 2.4e-4)
+    bt.cache.check()
+    bt.cache.close()
 
 
 @pytest.mark.parametrize("fmt", [rq.RQ_FMT_RESIDUAL, rq.RQ_FMT_BF16])
