@@ -1042,7 +1042,7 @@ __global__ void __launch_bounds__(kThreads, GK == 1 ? RQ_DECODE_MIN_CTAS : 3) de
             const size_t trow = ((size_t)b * a.tail_cap * a.H + h) * kHeadDim;
             const auto tail_k = a.tail_k ? a.tail_k + trow : nullptr, tail_v = a.tail_v ? a.tail_v + trow : nullptr;
             if (WIN) {
-                const size_t io = (size_t)b * a.ldq + hq0 + gq;
+                const size_t io = row + (size_t)(b * (a.ldq - a.Hq));
                 combine_row(a.partials + row * a.splits_max * kPartialStride, a.S, a.q + io * kHeadDim, a.scale_log2,
                             tail_k, tail_v, (size_t)a.H * kHeadDim, a.n_tail,
                             a.out16 ? nullptr : a.out + io * kHeadDim, tid, &s_red[0][0], ConsumerSync(),
