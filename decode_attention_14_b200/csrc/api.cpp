@@ -904,10 +904,7 @@ int rq_decode_attn_bf16(rq_cache *c, int layer, int loop, const void *q, float *
 namespace {
 
 // bytes of rebuilt rows a call keeps at once (more only if one kv head's rows are)
-#ifndef RQ_REBUILD_MAX
-#define RQ_REBUILD_MAX (size_t(4) << 30)
-#endif
-constexpr size_t kRebuildMax = RQ_REBUILD_MAX;
+constexpr size_t kRebuildMax = size_t(4) << 30;
 
 bool capturing(cudaStream_t st) {
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;

@@ -56,19 +56,11 @@ namespace {
 
 constexpr float kRsqrtD = 0.088388347648318440f;   // 1 / sqrt(128)
 constexpr int kWarps = 4;                          // warps per CTA
-#ifndef RQ_READ_CTAS
-#define RQ_READ_CTAS 4
-#endif
+constexpr int kCtas = 4;                           // CTAs per SM
 static_assert(32 * kWarps == kHeadDim, "a thread per sign");
 constexpr int kRecs = 16;                          // records of a tile
-#ifndef RQ_READ_TILES
-#define RQ_READ_TILES 4
-#endif
-#ifndef RQ_READ_SLOTS
-#define RQ_READ_SLOTS 4
-#endif
-constexpr int kTiles = RQ_READ_TILES;              // tiles per warp of a large call
-constexpr int kSlots = RQ_READ_SLOTS;              // ring slots per warp: kSlots - 1 steps in flight
+constexpr int kTiles = 4;                          // tiles per warp of a large call
+constexpr int kSlots = 4;                          // ring slots per warp: kSlots - 1 steps in flight
 
 // d = a b + c on the tensor cores: a 16 x 16, b 16 x 8, BF16, fp32 sums.
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2],
@@ -84,12 +76,9 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 // set-up and overlap, as long as four rounds of the 16 warps an SM holds remain
 // to even out the end: at 8k b4 (residual) 99 / 104 / 119 us with 4 / 2 / 1, at
 // 15 000 tiles 24.4 / 21.1 / 21.2 us.
-#ifndef RQ_ROUNDS
-#define RQ_ROUNDS 4
-#endif
 inline int warp_tiles(long long tiles) {
     int per = kTiles;
-    while (per > 1 && tiles < 148LL * 16 * RQ_ROUNDS * per) per /= 2;
+    while (per > 1 && tiles < 148LL * 16 * 4 * per) per /= 2;
     return per;
 }
 
@@ -263,7 +252,7 @@ __device__ __forceinline__ void pair_rest(const ReadArgs &a, const Span &s, cons
 // NR: residual records read, 0 or 1 (the shared reference), or 2 for any
 // number (a.nr, the chained reference).
 template <int BA, int BR, int GS, int NR, bool ROT, int OUT>
-__global__ void __launch_bounds__(32 * kWarps, NR == 2 ? 3 : RQ_READ_CTAS) read_rq_kernel(const ReadArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, NR == 2 ? 3 : kCtas) read_rq_kernel(const ReadArgs a) {
     using S = Slot<BA, BR>;
     const int nr = NR < 2 ? NR : a.nr;
     extern __shared__ __align__(16) uint8_t smem[];
