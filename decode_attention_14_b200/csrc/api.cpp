@@ -969,7 +969,7 @@ int plan_rebuild(rq_cache *c, const PrefillArgs &a, cudaStream_t st, ReadArgs *r
         rows = std::max(rows, rebuilt_rows(a.seqT.v[b] + a.n_tail, a.n, a.window, a.sinks).rows(a.seqT.v[b] + a.n_tail));
     rows = (rows + 15) / 16 * 16 + 128;   // a reader's tile may begin at the last row
     const size_t head = (size_t)a.B * rows * kHeadDim;   // elements of one part of one kv head
-    const int parts = a.out16 ? 2 : 4;                   // K and V; fp32 output: high and low
+    const int parts = a.out16 ? 3 : 4;                   // K in two; V in two for fp32 output
     const int heads = (int)std::min<size_t>(a.H, std::max<size_t>(1, kRebuildMax / (head * 2 * parts)));
     const size_t part = head * heads;
     const int s = grow_buffer(c, (void **)&c->rebuild_ws, &c->rebuild_bytes, part * 2 * parts, st);
@@ -987,7 +987,7 @@ int plan_rebuild(rq_cache *c, const PrefillArgs &a, cudaStream_t st, ReadArgs *r
     r->tail[1] = a.tail_v;
     for (int kv = 0; kv < 2; kv++) {
         r->out[kv] = c->rebuild_ws + kv * part;
-        r->out_lo[kv] = parts == 4 ? c->rebuild_ws + (2 + kv) * part : nullptr;
+        r->out_lo[kv] = 2 + kv < parts ? c->rebuild_ws + (2 + kv) * part : nullptr;
     }
     r->pair_stride = rows;
     r->pair_rows = rows;

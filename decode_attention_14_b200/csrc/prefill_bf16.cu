@@ -6,7 +6,7 @@
 //   z = q K^T scale,  out = sum_t 2^(z_t - m) v_t / sum_t 2^(z_t - m)
 // in one pass over the keys, with a running maximum m that is raised only when
 // a row's maximum grows by more than 2^8 (then the row's accumulated output is
-// rescaled), as in prefill.cuh.
+// rescaled).
 //
 // CTA = (split of the tokens, kv head, sequence x block of QT * 128 query rows,
 // row = query token x head of the group).  Per 128-token tile and 128 rows, on
@@ -15,7 +15,7 @@
 //   O += P V    8 MMAs of 128x128x16 with P from tensor memory, for each of P's
 //               PP BF16 parts: one for BF16 output (half a step, 2^-9 of each
 //               weight, is as small as the output's own rounding), a high and
-//               a low one for fp32 output (2^-17; a third one did not lower the
+//               a low one for fp32 output (2^-18; a third one did not lower the
 //               3e-6 that the tensor cores' sums leave)
 // P overwrites S in tensor memory; O is beside it (128 columns each).  Two S
 // buffers keep the tensor cores and the softmax busy at once: with QT = 2 one
@@ -38,13 +38,15 @@
 //             rescaled with QT = 1, and at the end)
 //
 // RB: the same over a compressed cache.  A first launch (rebuild.cu) writes the
-// tokens that the chunk sees, committed and tail, as FP16 into a workspace, once
-// for all the chunk's rows, and every product is in FP16 with K and V scaled by
-// 2^-8 and q by 2^-4: for BF16 output one part each of K, V and P (2^-12, below
-// the output's own rounding), for fp32 output two: S = Q (Khi + Klo)^T,
-// O += (Phi + Plo) Vhi + Phi Vlo.  (With BF16 operands the error of BF16 output
-// asks for two parts of K: 500 tokens in two sequences of 4 kv heads of 4 heads,
-// window 2000, 42 instead of 38 us, and half as much workspace again.)
+// tokens that the chunk sees, committed and tail, into a workspace, once for all
+// the chunk's rows, as pairs of BF16 numbers: S = Q (Khi + Klo)^T and, for fp32
+// output, O += (Phi + Plo) Vhi + Phi Vlo; for BF16 output one part of V and of P.
+// What is left out of a number is relative to it (2^-18 of a pair, 2^-9 of one),
+// whatever its size: FP16 operands would be faster (11 bits in one part: 37, 38
+// and 54 us for the cases below instead of 41, 41 and 63), but under any one scale
+// small values, and weights below 2^-25 of the largest, would be lost.  (V in
+// pairs for BF16 output too: 45, 53 and 70 us, the rows' relative error 2.1 to
+// 2.2e-3 instead of 2.2 to 2.7e-3; the output's own rounding makes 1.65e-3.)
 //
 // What bounds it: a full chunk is bound by the softmax between the two products
 // (one exponential and about six other operations per logit in a thread per
@@ -52,8 +54,9 @@
 // tensor pipe 36% and special-function pipe 37% busy in a 4096-token run.  Few
 // rows over a short window are bound by launches and the pipeline's filling:
 // 511 tokens in two sequences of 4 kv heads of 4, window 1024 (8.6 GFLOP), 30 us.
-// Over compressed caches (all launches), window 1024: 2048 tokens of 16 heads,
-// 54 us; 16 tokens of 4 x 16 heads, 37 us; the first launch takes about 20 of each.
+// Over compressed caches (all launches, BF16 output): 16 tokens of 4 x 16 heads,
+// window 1024, 41 us; 500 tokens in two sequences of 4 kv heads of 4 heads, window
+// 2000, 41 us; 2048 tokens of 16 heads, window 1024, 63 us.
 //
 // A V row that only some rows see may hold NaN or infinities, which 0 * NaN
 // would carry into the other rows.  The store kernel notes in the arena when it
@@ -156,15 +159,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float x0, float x1) {   // x0 in t
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(x1), "f"(x0));
     return d;
 }
-__device__ __forceinline__ uint32_t pack_f16(float x0, float x1) {
-    const __half2 h = __floats2half2_rn(x0, x1);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ float2 unpack_f16(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2 *>(&w)); }
-constexpr float kQScale = 1.f / 16.f;   // of q in FP16: up to 1e6
-__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w) {
-    return pack_f16(__uint_as_float(w << 16) * kQScale, __uint_as_float(w & 0xFFFF0000u) * kQScale);
-}
 // bits [lo, hi) of a 32-bit word (clamped)
 __device__ __forceinline__ uint32_t range_bits(int lo, int hi) {
     lo = max(lo, 0);
@@ -187,7 +181,7 @@ struct Bf16Args {
     float scale_log2;
 };
 
-// Tensor maps: K and V (RB: the rebuilt rows), and with two parts the low ones.
+// Tensor maps: K and V (RB: the rebuilt rows' high parts, and their low ones).
 struct Maps {
     CUtensorMap k, v, k_lo, v_lo;
 };
@@ -235,13 +229,13 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, 1)
     // this split's tiles
     const int j0 = (int)((long long)split * runs.tiles / a.S), j1 = (int)((long long)(split + 1) * runs.tiles / a.S);
     const int nt = j1 - j0;
-    // stages of tile j of the split: K, V, under RB each in PP parts
-    constexpr int KP = RB ? PP : 1;
+    // stages of tile j of the split: K in KP parts, V in VP
+    constexpr int KP = RB ? 2 : 1, VP = RB ? PP : 1;
     // S buffer of row tile q's token tile j, and the parity of its phase then
     auto sbuf = [](int q, int j) { return QT == 2 ? q : j & 1; };
     auto sphase = [](int j) { return QT == 2 ? j & 1 : (j >> 1) & 1; };
-    auto kstage = [](int j) { return 2 * KP * j; };
-    auto vstage = [](int j) { return 2 * KP * j + KP; };
+    auto kstage = [](int j) { return (KP + VP) * j; };
+    auto vstage = [](int j) { return (KP + VP) * j + KP; };
 
     if (tid == 0) {
         for (int i = 0; i < NS; i++) {
@@ -267,12 +261,6 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, 1)
         if (row < nr) {
             const int rg = r0 + row, t = rg / a.G, gq = rg % a.G;
             v = __ldg(reinterpret_cast<const uint4 *>(a.q + (((size_t)b * a.n + t) * a.Hq + h * a.G + gq) * kHeadDim) + c);
-            if (RB) {   // FP16 times 2^-4
-                v.x = bf16x2_to_f16x2(v.x);
-                v.y = bf16x2_to_f16x2(v.y);
-                v.z = bf16x2_to_f16x2(v.z);
-                v.w = bf16x2_to_f16x2(v.w);
-            }
         }
         *reinterpret_cast<uint4 *>(sm + (row / kTileR) * kStageBytes + (c >> 3) * kBlkBytes +
                                    tc::sw_chunk(row % kTileR, c & 7)) = v;
@@ -317,7 +305,7 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, 1)
                 load(&maps.k, y);
                 if (KP > 1) load(&maps.k_lo, y);
                 load(&maps.v, y);
-                if (KP > 1) load(&maps.v_lo, y);
+                if (VP > 1) load(&maps.v_lo, y);
             }
             // every issued load must have landed before the CTA exits
             for (int i = max(0, it - NS); i < it; i++) mbar_wait<256>(&bar_full[i % NS], (i / NS) & 1, abort_flag);
@@ -326,10 +314,8 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, 1)
     } else if (warp == 4 * QT + 1) {
         // ------------------------------------------------------- MMA
         if (lane == 0) {
-            // (operand formats, bits 7-9 and 10-12: 1 BF16, 0 FP16)
-            constexpr uint32_t fmt = RB ? (1u << 7) | (1u << 10) : 0u;
-            constexpr uint32_t idS = tc::idesc_bf16(kTileR, kTileT, false) & ~fmt;    // K: K-major
-            constexpr uint32_t idO = tc::idesc_bf16(kTileR, kHeadDim, true) & ~fmt;   // V: MN-major
+            constexpr uint32_t idS = tc::idesc_bf16(kTileR, kTileT, false);    // K: K-major
+            constexpr uint32_t idO = tc::idesc_bf16(kTileR, kHeadDim, true);   // V: MN-major
             auto logits = [&](int q, int j) {
                 const uint64_t da = tc::desc_k(sbase + q * kStageBytes);
 #pragma unroll
@@ -347,7 +333,7 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, 1)
             };
             auto values = [&](int q, int j) {
                 // P's parts against V, then its high part against V's low one
-                constexpr int terms = PP + KP - 1;
+                constexpr int terms = PP + VP - 1;
 #pragma unroll
                 for (int p = 0; p < terms; p++) {
                     const int s = (vstage(j) + (p == PP ? 1 : 0)) % NS;
@@ -363,7 +349,7 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, 1)
             };
             auto loaded = [&](int i, int code) { return wait(&bar_full[i % NS], (i / NS) & 1, code); };
             auto k_loaded = [&](int j) { return loaded(kstage(j), 32) && (KP == 1 || loaded(kstage(j) + 1, 33)); };
-            auto v_loaded = [&](int j) { return loaded(vstage(j), 34) && (KP == 1 || loaded(vstage(j) + 1, 35)); };
+            auto v_loaded = [&](int j) { return loaded(vstage(j), 34) && (VP == 1 || loaded(vstage(j) + 1, 35)); };
             // logits run AHEAD tiles before values: with QT = 1 into the other S buffer
             constexpr int AHEAD = QT == 2 ? 1 : 2;
             bool ok = true;
@@ -399,7 +385,7 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, 1)
         const int lo = (int)max(0ll, (long long)pos + 1 - a.window);
         const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16), tO = lanes + 256 + q * 128;
         const bool careful = __ldcg(a.nonfinite) != 0;
-        const float scale_log2 = RB ? a.scale_log2 * (1.f / (kQScale * kRebuildScale)) : a.scale_log2;
+        const float scale_log2 = a.scale_log2;
         float m_used = -CUDART_INF_F, l = 0.f;
         for (int j = 0; j < nt; j++) {
             const int tb = runs.token(j0 + j);
@@ -416,7 +402,7 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, 1)
                     const int s = vstage(j) % NS, t = tid;
                     wait(&bar_full[s], (vstage(j) / NS) & 1, 37);
                     const int s_lo = (vstage(j) + 1) % NS;
-                    constexpr bool has_lo = KP > 1;
+                    constexpr bool has_lo = VP > 1;
                     if (has_lo) wait(&bar_full[s_lo], ((vstage(j) + 1) / NS) & 1, 37);
                     uint32_t bad = 0;
                     for (int c = 0; c < 16; c++) {
@@ -425,7 +411,7 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, 1)
                         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                         for (int i = 0; i < 4; i++)   // exponents all ones
-                            bad |= (RB ? (w[i] & 0x7C007C00u) + 0x04000400u : (w[i] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+                            bad |= ((w[i] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
                     }
                     if (bad)
                         for (int c = 0; c < (has_lo ? 32 : 16); c++)
@@ -506,12 +492,9 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, 1)
                         p0 = ex2f(p0);
                         p1 = ex2f(p1);
                         sum[k & 3] = add2(sum[k & 3], pack2(p0, p1));
-                        hi[k] = RB ? pack_f16(p0, p1) : pack_bf16(p0, p1);
-                        if (PP > 1) {
-                            const float2 f = RB ? unpack_f16(hi[k])
-                                                : make_float2(__uint_as_float(hi[k] << 16), __uint_as_float(hi[k] & 0xFFFF0000u));
-                            low[k] = RB ? pack_f16(p0 - f.x, p1 - f.y) : pack_bf16(p0 - f.x, p1 - f.y);
-                        }
+                        hi[k] = pack_bf16(p0, p1);
+                        if (PP > 1)
+                            low[k] = pack_bf16(p0 - __uint_as_float(hi[k] << 16), p1 - __uint_as_float(hi[k] & 0xFFFF0000u));
                     }
                     __syncwarp();
                     st32(tS + 32 * c, hi);
@@ -538,8 +521,7 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, 1)
             const int rg = r0 + row, t = rg / a.G, gq = rg % a.G;
             const size_t prow = ((size_t)b * a.n + t) * a.Hq + h * a.G + gq;
             float *part = a.partials + (prow * a.S + split) * kPartialStride;
-            const float back = RB ? 1.f / kRebuildScale : 1.f;   // O holds V's scale
-            const float inv = l == 0.f ? 0.f : back / l;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
             for (int c = 0; c < 4; c++) {
                 uint32_t v[32];
@@ -556,8 +538,8 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, 1)
 #pragma unroll
                         for (int k = 0; k < 32; k += 4)
                             *reinterpret_cast<float4 *>(part + 32 * c + k) =
-                                make_float4(__uint_as_float(v[k]) * back, __uint_as_float(v[k + 1]) * back,
-                                            __uint_as_float(v[k + 2]) * back, __uint_as_float(v[k + 3]) * back);
+                                make_float4(__uint_as_float(v[k]), __uint_as_float(v[k + 1]), __uint_as_float(v[k + 2]),
+                                            __uint_as_float(v[k + 3]));
                     } else if (a.out16) {
 #pragma unroll
                         for (int k = 0; k < 32; k += 8) {
@@ -651,15 +633,15 @@ EncodeFn encode_fn() {
     return fn;
 }
 
-// [heads][rows][128] 16-bit numbers (a BF16 cache's K or V with rows = Tp, or
-// rebuilt rows in FP16): boxes of 128 rows x 64 elements, 128-byte swizzled;
+// [heads][rows][128] BF16 numbers (a BF16 cache's K or V with rows = Tp, or a
+// part of the rebuilt rows): boxes of 128 rows x 64 elements, 128-byte swizzled;
 // rows past the last read as zeros.
-bool make_map(CUtensorMap *map, const void *base, bool f16, long long rows, long long heads) {
+bool make_map(CUtensorMap *map, const void *base, long long rows, long long heads) {
     const EncodeFn fn = encode_fn();
     const cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)rows, (cuuint64_t)heads};
     const cuuint64_t strides[2] = {kHeadDim * 2, (cuuint64_t)rows * kHeadDim * 2};
     const cuuint32_t box[3] = {64, kTileT, 1}, step[3] = {1, 1, 1};
-    return fn && fn(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base),
+    return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base),
                     dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -787,7 +769,7 @@ cudaError_t launch_prefill_bf16(const PrefillArgs &p, const uint16_t *k, const u
     Maps m;
     std::memset(&m, 0, sizeof(m));
     const long long heads = (long long)p.B * p.H;
-    if (!make_map(&m.k, k, false, p.Tp, heads) || !make_map(&m.v, v, false, p.Tp, heads)) return cudaErrorInvalidValue;
+    if (!make_map(&m.k, k, p.Tp, heads) || !make_map(&m.v, v, p.Tp, heads)) return cudaErrorInvalidValue;
     return launch_plain(p.row_tiles, m, bf16_args(p, nonfinite), st);
 }
 
@@ -795,9 +777,9 @@ cudaError_t launch_prefill_rebuilt(const PrefillArgs &p, const ReadArgs &r, cuda
     Maps m;
     std::memset(&m, 0, sizeof(m));
     const long long heads = (long long)p.B * r.H;
-    if (!make_map(&m.k, r.out[0], true, r.pair_stride, heads) || !make_map(&m.v, r.out[1], true, r.pair_stride, heads) ||
-        (r.out_lo[0] && (!make_map(&m.k_lo, r.out_lo[0], true, r.pair_stride, heads) ||
-                         !make_map(&m.v_lo, r.out_lo[1], true, r.pair_stride, heads))))
+    if (!make_map(&m.k, r.out[0], r.pair_stride, heads) || !make_map(&m.v, r.out[1], r.pair_stride, heads) ||
+        !make_map(&m.k_lo, r.out_lo[0], r.pair_stride, heads) ||
+        (r.out_lo[1] && !make_map(&m.v_lo, r.out_lo[1], r.pair_stride, heads)))
         return cudaErrorInvalidValue;
     Bf16Args a = bf16_args(p, r.nonfinite);
     a.h0 = r.h0;

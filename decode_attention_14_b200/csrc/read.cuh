@@ -41,10 +41,10 @@
 // elements per instruction), rounded once to the output's type.
 //
 // kOutPair (rebuild.cu) writes the rows that a chunk of new tokens attends to,
-// the tail's among them, as FP16 into a workspace for the tensor-core attention
-// of prefill_bf16.cu: one FP16 number each (2^-12) for BF16 output, a high and a
-// low one (2^-23) for fp32 output; sequence by sequence the rows that
-// rebuilt_rows() names.
+// the tail's among them, into a workspace for the tensor-core attention of
+// prefill_bf16.cu: a value as the BF16 number next to it and a second one for
+// what that leaves (2^-18 of the value is lost; V for BF16 output: the first
+// alone, 2^-9); sequence by sequence the rows that rebuilt_rows() names.
 #pragma once
 
 #include "common.cuh"
@@ -208,19 +208,23 @@ __device__ __forceinline__ void expand4(const uint8_t *row, int sg, int q, float
 __device__ __forceinline__ long long pair_at(const ReadArgs &a, const Span &s, int i) {
     return (((long long)s.b * a.H + s.h) * a.pair_stride + i) * kHeadDim;
 }
-// Writes four values; nonzero if one of them is a V that is not finite (in FP16).
-__device__ __forceinline__ uint32_t store_pair(const ReadArgs &a, int kv, long long at, const float (&v)[4]) {
-    const float x[4] = {v[0] * kRebuildScale, v[1] * kRebuildScale, v[2] * kRebuildScale, v[3] * kRebuildScale};
-    const __half2 h0 = __floats2half2_rn(x[0], x[1]), h1 = __floats2half2_rn(x[2], x[3]);
+// Writes four values; nonzero if one of them is a V that is not finite.
+__device__ __forceinline__ uint32_t store_pair(const ReadArgs &a, int kv, long long at, const float (&x)[4]) {
+    const __nv_bfloat162 h0 = __floats2bfloat162_rn(x[0], x[1]), h1 = __floats2bfloat162_rn(x[2], x[3]);
     const uint2 hi = make_uint2(*reinterpret_cast<const uint32_t *>(&h0), *reinterpret_cast<const uint32_t *>(&h1));
     *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out[kv]) + at) = hi;
+    // exponents all ones
+    const uint32_t bad = (((hi.x & 0x7F807F80u) + 0x00800080u) | ((hi.y & 0x7F807F80u) + 0x00800080u)) & 0x80008000u;
     if (a.out_lo[kv]) {   // uniform
-        const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
-        const __half2 l0 = __floats2half2_rn(x[0] - f0.x, x[1] - f0.y), l1 = __floats2half2_rn(x[2] - f1.x, x[3] - f1.y);
+        const __nv_bfloat162 l0 =
+            __floats2bfloat162_rn(x[0] - __uint_as_float(hi.x << 16), x[1] - __uint_as_float(hi.x & 0xFFFF0000u));
+        const __nv_bfloat162 l1 =
+            __floats2bfloat162_rn(x[2] - __uint_as_float(hi.y << 16), x[3] - __uint_as_float(hi.y & 0xFFFF0000u));
+        // (beside an infinity nothing: it would be an infinity less itself)
         *reinterpret_cast<uint2 *>(a.out_lo[kv] + at) =
-            make_uint2(*reinterpret_cast<const uint32_t *>(&l0), *reinterpret_cast<const uint32_t *>(&l1));
+            bad ? make_uint2(0u, 0u) : make_uint2(*reinterpret_cast<const uint32_t *>(&l0), *reinterpret_cast<const uint32_t *>(&l1));
     }
-    return kv == 0 ? 0u : (((hi.x & 0x7C007C00u) + 0x04000400u) | ((hi.y & 0x7C007C00u) + 0x04000400u)) & 0x80008000u;
+    return kv == 0 ? 0u : bad;
 }
 // The span's rows beside those with records: the tail's tokens, and zero rows
 // past the sequence's end (a reader's tile of 128 rows ends there).

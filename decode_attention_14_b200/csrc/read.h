@@ -28,12 +28,11 @@ struct ReadArgs {
     int g;
     int rotate;
     uint32_t sigma[4];
-    // launch_rebuild: FP16 rows times kRebuildScale, `out` [B * H][pair_stride][d]
-    // (their high parts where out_lo takes the low ones); pair_rows rows (a
-    // multiple of 16) of every sequence are written, zeros past its rebuilt
-    // ones; n, n_tail, window and sinks are the attention call's.  *nonfinite is
-    // set to 1 when a V value is not finite in FP16.  The kv heads are
-    // [h0, h0 + H) of H_all.
+    // launch_rebuild: rows as pairs of BF16 numbers, the high ones in `out`
+    // [B * H][pair_stride][d], the low ones in `out_lo` (null: left out); pair_rows rows (a multiple of 16) of every sequence are written,
+    // zeros past its rebuilt ones; n, n_tail, window and sinks are the attention
+    // call's.  *nonfinite is set to 1 when a V value is not finite.  The kv heads
+    // are [h0, h0 + H) of H_all.
     uint16_t *out_lo[2];
     int h0, H_all;
     long long pair_stride;
@@ -41,10 +40,6 @@ struct ReadArgs {
     int window, sinks;
     int *nonfinite;
 };
-
-// FP16 holds the rebuilt values times 2^-8: up to 1.6e7, with 11 bits down to
-// 0.016 and steps of 1.5e-5 below.
-constexpr float kRebuildScale = 1.f / 256.f;
 
 // The positions that n new tokens of a windowed call see between them, of a
 // sequence of `end` tokens: the sinks (rows 0 .. sink_pad - 1 of the workspace,

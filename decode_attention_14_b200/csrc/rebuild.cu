@@ -1,5 +1,5 @@
 // rebuild.cu -- the rows that a chunk of new tokens attends to, rebuilt from the
-// compressed cache in FP16 in a workspace (the first launch of
+// compressed cache as BF16 pairs in a workspace (the first launch of
 // rq_prefill_attn_window): the kOutPair instantiations of read.cuh.  The chunk's
 // rows share this work, which a fused kernel would repeat for every block of 64
 // of them (500 / 2048 tokens 147 / 250 us fused, 38 / 54 us with the workspace).

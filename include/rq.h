@@ -316,13 +316,13 @@ int rq_decode_attn_window(rq_cache *cache, int layer, int loop, const void *q_bf
  * rq_decode_attn_window does (n_tokens, the heads per kv head and the number of
  * visible tokens decide).  Else: products on the tensor cores with fp32 sums.  BF16 caches: exact
  * products of q and K; the weights are BF16 for BF16 output (half a step, 2^-9,
- * of each weight beside the output's own rounding), two BF16 parts (2^-17) for
- * fp32 output.  Compressed caches: the visible rows are rebuilt as FP16 (times
- * 2^-8, q times 2^-4), one number each for BF16 output (2^-12), two for fp32
- * output (2^-23); |k|, |v| >= 1.6e7 and |q| >= 1e6 count as not finite there.
+ * of each weight beside the output's own rounding), two BF16 parts (2^-18) for
+ * fp32 output.  Compressed caches: the same with the visible rows rebuilt in two
+ * BF16 parts (2^-18), V in one for BF16 output (2^-9).  All of these are relative
+ * to the number itself, whatever its size.
  * Buffers the cache allocates on the first call and grows when a later call
  * needs more: split partials, and for compressed caches the rebuilt rows:
- * batch * (tokens visible to any of the n, + 143 at most) * 512 bytes a kv head
+ * batch * (tokens visible to any of the n, + 143 at most) * 768 bytes a kv head
  * (1024 with fp32 output), for as many kv heads at a time as 4 GiB hold, at
  * least one.  Growing synchronises the device and cannot be done while `stream`
  * is being captured (NOMEM, the capture stays valid): make the first call of a

@@ -1,0 +1,124 @@
+"""Values at the ends of the range for the windowed attention calls: small and
+large numbers, weights far below the largest, tokens that are not finite, and
+buffers that grow with the visible tokens.  The reference is a softmax in 64
+bits over what the cache holds, read back in fp32 (a record's value in fp32 is
+within a few 2^-24 of itself).
+
+Tolerances, of each output row's norm.  fp32 output: a row and its weight are
+two BF16 numbers each, off by at most half a step of the second, 2^-18: at
+random signs over 128 products and over the tokens that is a few 1e-6 of the
+logits and of the row, and the tensor cores' sums leave up to 3.5e-6: 2e-5.
+BF16 output: half a step, 2^-9 of each element, and 2^-9 of each weight: 2^-8.
+"""
+import numpy as np
+import pytest
+import torch
+
+import decode_attention_14_b200 as rq
+import synth
+
+import rqharness as H
+
+pytestmark = pytest.mark.gpu
+TOL = {torch.float32: 2e-5, torch.bfloat16: 2.0 ** -8}
+
+
+def make(B=1, heads=2, Hq=2, Lg=4, max_tokens=512, tail=256, fmt=rq.RQ_FMT_RESIDUAL, **kw):
+    return H.guarded_cache(rq.make_config(num_layers=1, num_loops=Lg, loops_per_group=Lg, batch=B, max_tokens=max_tokens,
+                                          max_tail_tokens=tail if fmt == rq.RQ_FMT_RESIDUAL else 0, num_kv_heads=heads,
+                                          num_q_heads=Hq, format=fmt, seed=0xA11CE, **kw))
+
+
+def normal(seed, *shape):
+    return torch.randn(shape, device="cuda", generator=torch.Generator("cuda").manual_seed(seed))
+
+
+def reference(k, v, q, window, sinks, scale=128 ** -0.5):
+    """k, v [B][P][H][d], q [B][n][Hq][d] -> [B][n][Hq][d] in 64 bits; tokens that no row sees may hold anything."""
+    k, v, q = k.double(), v.double(), q.double()
+    P, n, G = k.shape[1], q.shape[1], q.shape[2] // k.shape[2]
+    pos = torch.arange(P - n, P, device="cuda")[:, None]
+    t = torch.arange(P, device="cuda")[None, :]
+    seen = (t <= pos) & ((t > pos - window) | (t < sinks)) if window else t <= pos
+    k, v = (torch.where(seen.any(0)[None, :, None, None], x, 0.0).repeat_interleave(G, 2) for x in (k, v))
+    z = torch.einsum("bihd,bjhd->bhij", q, k) * scale
+    return torch.einsum("bhij,bjhd->bihd", torch.softmax(z.masked_fill(~seen, -float("inf")), -1), v)
+
+
+def close(got, ref, tol):
+    """Every row within tol of its norm."""
+    far = (got.double() - ref).norm(dim=-1) / ref.norm(dim=-1)
+    assert bool((far <= tol).all()), far.max().item()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("size", [3e3, 1.0, 1e-2, 1e-4, 1e-6, 1e-12])
+def test_chunks_over_values_of_any_size(size, dtype):
+    """Tail rows of one size after committed ones of about 1: windows that see the tail alone, and both."""
+    cache = make(B=2, heads=2, Hq=4)
+    for j in range(4):
+        cache.append(0, j, normal(j, 2, 100, 2, 128).bfloat16(), normal(9 + j, 2, 100, 2, 128).bfloat16())
+    k, v = (normal(s, 2, 60, 2, 128) * size for s in (20, 21))
+    cache.append(0, 1, (k if size < 10 else k / size).bfloat16(), v.bfloat16())     # (a large K leaves one token of a row)
+    kr, vr = cache.read(0, 1, dtype=torch.float32)
+    q = normal(22, 2, 40, 4, 128).bfloat16()
+    for window, sinks in ((8, 0), (20, 0), (64, 0), (20, 5), (0, 0)):
+        close(cache.prefill_window(0, 1, q, window, sinks, dtype=dtype), reference(kr, vr, q, window, sinks), TOL[dtype])
+    cache.check()
+    cache.close()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("size", [1e-3, 1e-2, 1.0, 30.0])
+def test_chunks_over_records_of_any_size(size, dtype):
+    """Committed rows, anchor and residual loops (FP8 scales reach down to 2^-9)."""
+    cache = make(heads=2, Hq=4, max_tokens=400)
+    for t in (0, 200):
+        for j in range(4):
+            cache.append(0, j, (normal(t + j, 1, 200, 2, 128) * min(size, 1.0)).bfloat16(),
+                         (normal(t + 9 + j, 1, 200, 2, 128) * size).bfloat16())
+    q = normal(23, 1, 50, 4, 128).bfloat16()
+    for loop in (0, 3):
+        kr, vr = cache.read(0, loop, dtype=torch.float32)
+        for window, sinks in ((30, 0), (150, 4), (0, 0)):
+            ref = reference(kr, vr, q, window, sinks)
+            got = cache.prefill_window(0, loop, q, window, sinks, dtype=dtype)
+            far = (got.double() - ref).norm() / ref.norm()      # (rows of records that are all zero have no norm)
+            assert far <= TOL[dtype], far.item()
+    cache.check()
+    cache.close()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+def test_chunk_queries_of_any_size(dtype):
+    """q and the scale moved by powers of two against one another: the same logits, so the same bits."""
+    cache = make(heads=2, Hq=4)
+    for j in range(4):
+        cache.append(0, j, normal(j, 1, 150, 2, 128).bfloat16(), normal(9 + j, 1, 150, 2, 128).bfloat16())
+    q = normal(24, 1, 40, 4, 128).bfloat16()
+    first = cache.prefill_window(0, 1, q, 70, 3, dtype=dtype, scale=2.0 ** -4)
+    for e in (-40, -20, 15, 30):
+        assert torch.equal(cache.prefill_window(0, 1, q * 2.0 ** e, 70, 3, dtype=dtype, scale=2.0 ** (-4 - e)), first), e
+    cache.close()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("at", [0, 4000])
+@pytest.mark.parametrize("below", [12.0, 17.5, 30.0])
+def test_weights_far_below_the_largest(below, at, dtype):
+    """One token's logit is `below` above all others', and its V is zero: the row is what the others' small weights make
+    of theirs."""
+    T, n = 8192, 40
+    cache = make(heads=1, Hq=1, Lg=1, max_tokens=T)
+    k, v = torch.zeros((1, T, 1, 128), device="cuda"), normal(31, 1, T, 1, 128) + 1.0
+    u = torch.sign(normal(32, 128))
+    k[0, at, 0], v[0, at, 0] = u, 0.0
+    cache.append(0, 0, k.bfloat16(), v.bfloat16())
+    kr, vr = cache.read(0, 0, dtype=torch.float32)
+    q = (u * below / 128 ** 0.5).expand(1, n, 1, 128).bfloat16().contiguous()
+    ref = reference(kr, vr, q, 0, 0)
+    far = (ref.norm(dim=-1) * np.exp(below) / T).min().item()
+    assert 1.0 < far, far                                   # the dominant token leaves the others e^-below each
+    close(cache.prefill_window(0, 0, q, 0, dtype=dtype), ref, TOL[dtype])
+    cache.check()
+    cache.close()
