@@ -889,10 +889,11 @@ __global__ void __launch_bounds__(kThreads, GK == 1 ? RQ_DECODE_MIN_CTAS : 3) de
                     for (int gq = 0; gq < GK; gq++) W[gq][k] = wsrc[gq * a.chunk + j * kItem + tok - sh * kTile];
                 }
                 // a masked token's records may hold anything: nothing of it times weight 0
-                if (WIN && (j * kItemTiles + u == sh || j * kItemTiles + u == ntv - 1)) {
+                const int tt = j * kItem + (u - sh) * kTile;   // the tile's first token
+                if (WIN && (tt + kTile > n || (tt < m1 && tt + kTile > m0))) {   // uniform
 #pragma unroll
                     for (int k = 0; k < 4; k++) {
-                        const int t = j * kItem + u * kTile + 16 * warp + sub + 4 * k - sh * kTile;
+                        const int t = tt + 16 * warp + sub + 4 * k;
                         if (t >= n || masked(t)) mm[k] = make_float2(0.f, 0.f);
                     }
                 }

@@ -283,7 +283,9 @@ int rq_prefill_attn(rq_cache *cache, int layer, int loop, const void *q_bf16, in
  *   q_bf16: device, [batch][num_q_heads][head_dim] BF16.
  *   out:    device, [batch][num_q_heads][head_dim] of out_type (rq_out_type).
  *   softmax_scale: as for rq_decode_attn.
- * Only the records of visible tokens (in whole 64-token tiles) are read;
+ * Only the records of visible tokens (in whole 64-token tiles) are read, except
+ * where both runs together fill the workspace's splits (sequences near 262144
+ * tokens, nearly all of them visible: the tokens between the runs are read too);
  * masked tokens do not enter the result, whatever they hold (the value weights'
  * fixed point of a compressed cache is relative to the largest FP8 scale ever
  * written to the stream, masked tokens' among them).  With no token at all the

@@ -122,3 +122,26 @@ def test_weights_far_below_the_largest(below, at, dtype):
     close(cache.prefill_window(0, 0, q, 0, dtype=dtype), ref, TOL[dtype])
     cache.check()
     cache.close()
+
+
+def test_masked_tokens_between_the_runs_of_one_split():
+    """Nearly the whole of the longest cache is visible: the sequence is dealt out as one, and whole tiles inside a split
+    are masked.  What they hold does not show."""
+    T, sinks, window = 262144, 1088, 260480
+    cache = make(heads=1, Hq=1, Lg=1, max_tokens=T)
+    clean = make(heads=1, Hq=1, Lg=1, max_tokens=T)
+    for t in range(0, T, 1 << 16):
+        k, v = (normal(t + i, 1, 1 << 16, 1, 128).bfloat16() for i in (1, 2))
+        clean.append(0, 0, k, v)
+        if t == 0:
+            k[:, sinks:T - window], v[:, sinks:T - window] = float("nan"), float("nan")
+        cache.append(0, 0, k, v)
+    q = normal(33, 1, 1, 128).bfloat16()
+    k, v = clean.read(0, 0, dtype=torch.float32)
+    ref = reference(k, v, q[:, None], window, sinks)[:, 0]
+    for dtype in TOL:
+        close(clean.decode_window(0, 0, q, window, sinks, dtype=dtype), ref, TOL[dtype])
+        close(cache.decode_window(0, 0, q, window, sinks, dtype=dtype), ref, TOL[dtype])
+    cache.check()
+    cache.close()
+    clean.close()
