@@ -214,6 +214,11 @@ def _check_dev(t, dtype_name: str, shape, what: str):
         raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
+def _check_aligned(t, what: str):
+    if t.data_ptr() % 16:
+        raise ValueError(f"{what} must be 16-byte aligned")
+
+
 def _out_type(dtype) -> int:
     import torch
     if dtype == torch.float32:
@@ -418,11 +423,13 @@ class Cache:
     @staticmethod
     def _window_out(out, dtype, shape, q):
         import torch
+        _check_aligned(q, "q")
         if out is None:
             return torch.empty(shape, dtype=dtype or torch.float32, device=q.device)
         if dtype is not None and out.dtype != dtype:
             raise ValueError(f"out is {out.dtype}, not {dtype}")
         _check_dev(out, "bfloat16" if out.dtype == torch.bfloat16 else "float32", shape, "out")
+        _check_aligned(out, "out")
         return out
 
     def prefill(self, layer: int, loop: int, q, out=None, scale: float = 0.0, stream=None):

@@ -289,6 +289,9 @@ bool rows_disjoint(int64_t nb, int64_t sb, int64_t nt, int64_t st, int64_t nh, i
     return true;
 }
 
+// The windowed calls' kernels read q and write out in whole 16-byte vectors.
+bool rows_aligned(const void *q, const void *out) { return ((uintptr_t)q | (uintptr_t)out) % 16 == 0; }
+
 float resolve_scale(float s) { return s > 0.f ? s : 1.0f / std::sqrt((float)kHeadDim); }
 
 // Kernels run on the current device and address the cache's arena, so the
@@ -1150,7 +1153,7 @@ extern "C" {
 int rq_decode_attn_window(rq_cache *c, int layer, int loop, const void *q, void *out, int out_type, float scale,
                           int window, int sinks, void *stream) {
     WindowSpec w;
-    if (!c || !window_spec(window, sinks, out_type, &w)) return RQ_ERR_INVALID;
+    if (!c || !window_spec(window, sinks, out_type, &w) || !rows_aligned(q, out)) return RQ_ERR_INVALID;
     const rq_config &cfg = c->lay.cfg;
     const bool bf16 = cfg.format == RQ_FMT_BF16;
     // heads in groups of four and more over a BF16 cache: the chunk's kernel, which reads K and V once for
@@ -1172,7 +1175,7 @@ int rq_prefill_attn(rq_cache *c, int layer, int loop, const void *q, int n, floa
 int rq_prefill_attn_window(rq_cache *c, int layer, int loop, const void *q, int n, void *out, int out_type, float scale,
                            int window, int sinks, void *stream) {
     WindowSpec w;
-    if (!c || !window_spec(window, sinks, out_type, &w)) return RQ_ERR_INVALID;
+    if (!c || !window_spec(window, sinks, out_type, &w) || !rows_aligned(q, out)) return RQ_ERR_INVALID;
     return prefill_common(c, layer, loop, q, n, out, scale, stream, &w);
 }
 

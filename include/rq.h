@@ -280,8 +280,9 @@ int rq_prefill_attn(rq_cache *cache, int layer, int loop, const void *q_bf16, in
  *   window: > 0; 0 for no window (every token; sinks is then ignored).  A
  *     window longer than the sequence is the whole sequence.
  *   sinks:  >= 0; may reach into the window.
- *   q_bf16: device, [batch][num_q_heads][head_dim] BF16.
- *   out:    device, [batch][num_q_heads][head_dim] of out_type (rq_out_type).
+ *   q_bf16: device, [batch][num_q_heads][head_dim] BF16, 16-byte aligned.
+ *   out:    device, [batch][num_q_heads][head_dim] of out_type (rq_out_type),
+ *     16-byte aligned.
  *   softmax_scale: as for rq_decode_attn.
  * Only the records of visible tokens (in whole 64-token tiles) are read, except
  * where both runs together fill the workspace's splits (sequences near 262144
@@ -295,8 +296,8 @@ int rq_prefill_attn(rq_cache *cache, int layer, int loop, const void *q_bf16, in
  * the arithmetic of rq_prefill_attn_window over such a cache, on the tensor
  * cores.  No buffer beyond the arena is used.  Overlap, workspace and stream
  * rules are rq_decode_attn's.
- * Errors: INVALID (null pointer, index, window < 0, sinks < 0, out_type),
- * UNSUPPORTED (as rq_decode_attn), CUDA.
+ * Errors: INVALID (null or unaligned pointer, index, window < 0, sinks < 0,
+ * out_type), UNSUPPORTED (as rq_decode_attn), CUDA.
  */
 int rq_decode_attn_window(rq_cache *cache, int layer, int loop, const void *q_bf16, void *out, int out_type,
                           float softmax_scale, int window, int sinks, void *stream);
@@ -309,8 +310,9 @@ int rq_decode_attn_window(rq_cache *cache, int layer, int loop, const void *q_bf
  * RQ_FMT_BF16 caches (whose appends commit at once: the n new tokens are the
  * last committed ones) it is also, with window 0, the plain causal attention
  * of a prefill chunk.
- *   q_bf16: device, [batch][n_tokens][num_q_heads][head_dim] BF16, oldest first.
- *   out:    device, the same shape, of out_type (rq_out_type).
+ *   q_bf16: device, [batch][n_tokens][num_q_heads][head_dim] BF16, oldest first,
+ *     16-byte aligned.
+ *   out:    device, the same shape, of out_type (rq_out_type), 16-byte aligned.
  *   window, sinks, softmax_scale: as for rq_decode_attn_window.
  * A masked token does not enter a row, whatever it holds; a row that sees a V
  * that is not finite is not finite either (from the tensor cores NaN as a whole).
@@ -331,8 +333,8 @@ int rq_decode_attn_window(rq_cache *cache, int layer, int loop, const void *q_bf
  * size before.  Buffers that a captured call uses stay until rq_cache_destroy,
  * also when outgrown.  Calls on one cache share them: calls whose work overlaps
  * (other streams, two replayed graphs) must be ordered by the caller.
- * Errors: INVALID (null pointer, n_tokens < 1, index, window < 0, sinks < 0,
- * out_type), STATE (a sequence holds fewer than n_tokens tokens), UNSUPPORTED
+ * Errors: INVALID (null or unaligned pointer, n_tokens < 1, index, window < 0,
+ * sinks < 0, out_type), STATE (a sequence holds fewer than n_tokens tokens), UNSUPPORTED
  * (as rq_prefill_attn, and more than 65535 row blocks of 128 query rows over
  * the batch), NOMEM, CUDA.
  */

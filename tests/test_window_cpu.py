@@ -26,3 +26,14 @@ def test_rows_must_be_cuda_tensors_of_a_known_type():
 def test_queries_must_be_contiguous_cuda_bfloat16():
     with pytest.raises(ValueError):
         rq._check_dev(torch.zeros((1, 2, 128), dtype=torch.bfloat16), "bfloat16", (1, 2, 128), "q")
+
+
+@pytest.mark.parametrize("offset,aligned", [(0, True), (1, False), (4, False), (8, True)])
+def test_rows_must_be_16_byte_aligned(offset, aligned):
+    t = torch.zeros(512, dtype=torch.bfloat16)
+    assert t.data_ptr() % 16 == 0
+    if aligned:
+        rq._check_aligned(t[offset:], "q")
+    else:
+        with pytest.raises(ValueError, match="16-byte"):
+            rq._check_aligned(t[offset:], "q")

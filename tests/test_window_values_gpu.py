@@ -145,3 +145,27 @@ def test_masked_tokens_between_the_runs_of_one_split():
     cache.check()
     cache.close()
     clean.close()
+
+
+@pytest.mark.parametrize("fmt,Hq", [(rq.RQ_FMT_RESIDUAL, 2), (rq.RQ_FMT_BF16, 2), (rq.RQ_FMT_BF16, 8)])
+def test_rows_off_their_alignment_are_refused(fmt, Hq):
+    """q or out at an odd element or 8 bytes on, contiguous all the same: refused before any launch, out as it was."""
+    cache = make(heads=2, Hq=Hq, Lg=1, fmt=fmt)
+    cache.append(0, 0, normal(61, 1, 50, 2, 128).bfloat16(), normal(62, 1, 50, 2, 128).bfloat16())
+    rows = normal(63, 9 * Hq * 128).bfloat16()
+    for n, call in ((1, cache.decode_window), (7, cache.prefill_window)):
+        shape = (1, Hq, 128) if n == 1 else (1, n, Hq, 128)
+        size = n * Hq * 128
+        for dtype in TOL:
+            space = torch.full((size + 16,), 7.0, dtype=dtype, device="cuda")
+            for qo, oo in ((1, 0), (4, 0), (0, 1), (0, 2), (3, 1)):
+                q, out = rows[qo:qo + size].view(shape), space[oo:oo + size].view(shape)
+                with pytest.raises(ValueError, match="aligned"):
+                    call(0, 0, q, 4, out=out)
+                args = (cache.h, 0, 0, q) + ((n,) if n > 1 else ()) + (out, rq._out_type(dtype), 0.0, 4, 0)
+                raw = rq.rq_decode_attn_window if n == 1 else rq.rq_prefill_attn_window
+                assert raw(*args) == rq.RQ_ERR_INVALID
+            torch.cuda.synchronize()
+            assert (space == 7.0).all()
+    cache.check()
+    cache.close()
