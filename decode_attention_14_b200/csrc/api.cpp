@@ -289,8 +289,9 @@ bool rows_disjoint(int64_t nb, int64_t sb, int64_t nt, int64_t st, int64_t nh, i
     return true;
 }
 
-// The windowed calls' kernels read q and write out in whole 16-byte vectors.
-bool rows_aligned(const void *q, const void *out) { return ((uintptr_t)q | (uintptr_t)out) % 16 == 0; }
+// Whether two arrays of rows can be read or written in vectors of `bytes` (the
+// windowed calls' kernels take q and out in whole 16-byte vectors).
+bool rows_aligned(const void *a, const void *b, size_t bytes = 16) { return ((uintptr_t)a | (uintptr_t)b) % bytes == 0; }
 
 float resolve_scale(float s) { return s > 0.f ? s : 1.0f / std::sqrt((float)kHeadDim); }
 
@@ -605,6 +606,8 @@ int rq_append(rq_cache *c, int layer, int loop, const void *k, const void *v, in
     const Layout &L = c->lay;
     const rq_config &cfg = L.cfg;
     if (layer < 0 || layer >= cfg.num_layers || loop < 0 || loop >= cfg.num_loops) return RQ_ERR_INVALID;
+    // copied in 16-byte vectors, read by the encoder in 8-byte ones
+    if (!rows_aligned(k, v, cfg.format != RQ_FMT_BF16 && is_commit_loop(L, loop) ? 8 : 16)) return RQ_ERR_INVALID;
     cudaStream_t st = (cudaStream_t)stream;
     if (cfg.format == RQ_FMT_BF16) {
         const size_t slot = (size_t)layer * cfg.num_loops + loop;
@@ -824,6 +827,7 @@ static int decode_common(rq_cache *c, int layer, int loop, const void *q, float 
             if (s != RQ_OK) return s;
             return decode_common(c, layer, loop, q, out, scale, stream, bf16);
         }
+        if (!rows_aligned(app_k, app_v)) return RQ_ERR_INVALID;
         int &nt = c->ntail[(size_t)layer * cfg.num_loops + loop];
         if (nt + app_n > L.tail_cap) return RQ_ERR_CAPACITY;
         const int group = loop / L.Lg, j = loop % L.Lg;
@@ -1169,6 +1173,7 @@ int rq_decode_attn_window(rq_cache *c, int layer, int loop, const void *q, void 
 }
 
 int rq_prefill_attn(rq_cache *c, int layer, int loop, const void *q, int n, float *out, float scale, void *stream) {
+    if (!rows_aligned(q, q, 8) || !rows_aligned(out, out)) return RQ_ERR_INVALID;
     return prefill_common(c, layer, loop, q, n, out, scale, stream, nullptr);
 }
 

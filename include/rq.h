@@ -170,7 +170,8 @@ int rq_cache_destroy(rq_cache *cache);
 
 /*
  * Append n_tokens tokens of one (layer, loop) for every sequence.
- *   k_bf16, v_bf16: device, [batch][n_tokens][num_kv_heads][head_dim] BF16.
+ *   k_bf16, v_bf16: device, [batch][n_tokens][num_kv_heads][head_dim] BF16,
+ *     16-byte aligned (INVALID otherwise; 8 bytes do at an anchor loop).
  * RQ_FMT_RESIDUAL:
  *   - a non-anchor loop copies its K/V into that loop's BF16 tail (the
  *     in-flight tokens, read by decode as they are);
@@ -240,8 +241,9 @@ int rq_decode_attn_bf16(rq_cache *cache, int layer, int loop, const void *q_bf16
  * (paragraph 4) times decode only; this call is the step before it, reading
  * the same records the decode reads.
  *   q_bf16: device, [batch][n_tokens][num_q_heads][head_dim] BF16: the n most
- *           recent tokens of every sequence, oldest first.
- *   out:    device, [batch][n_tokens][num_q_heads][head_dim] fp32.
+ *           recent tokens of every sequence, oldest first; 8-byte aligned.
+ *   out:    device, [batch][n_tokens][num_q_heads][head_dim] fp32, 16-byte
+ *           aligned.
  *   softmax_scale: as for rq_decode_attn.
  * Keys/values: the sequence of the loop's group's committed tokens (as
  * rq_decode_attn reconstructs them) followed by the loop's BF16 tail tokens;
@@ -259,7 +261,7 @@ int rq_decode_attn_bf16(rq_cache *cache, int layer, int loop, const void *q_bf16
  * device, so make the first call of a size before any stream capture.  Calls
  * on one cache share the buffers: calls whose work overlaps (other streams)
  * must be ordered by the caller.
- * Errors: INVALID (null pointer, n_tokens < 1, index out of range), STATE
+ * Errors: INVALID (null or unaligned pointer, n_tokens < 1, index out of range), STATE
  * (wrong format, or a sequence holds fewer than n_tokens tokens),
  * UNSUPPORTED (n_tokens > 65535, an INT2 anchor with INT4 residuals -- the
  * multi-token kernel is built for INT4/INT2, INT2/INT2 and INT4/INT4 -- or

@@ -169,3 +169,35 @@ def test_rows_off_their_alignment_are_refused(fmt, Hq):
             assert (space == 7.0).all()
     cache.check()
     cache.close()
+
+
+def test_appended_rows_off_their_alignment_are_refused():
+    """k, v of an append (also the fused one) and q, out of rq_prefill_attn: refused before any launch, nothing appended."""
+    cache = make(heads=2, Hq=2)
+    bf = make(heads=2, Hq=2, Lg=1, fmt=rq.RQ_FMT_BF16)
+    for j in range(4):
+        cache.append(0, j, normal(j, 1, 20, 2, 128).bfloat16(), normal(9 + j, 1, 20, 2, 128).bfloat16())
+    rows = normal(64, 9 * 2 * 128).bfloat16()
+    at = lambda o, n=3: rows[o:o + n * 256].view(1, n, 2, 128)      # noqa: E731
+    q, out = at(0, 1)[:, 0], torch.full((1, 2, 128), 7.0, device="cuda")
+    for off in (1, 2, 4):
+        for k, v in ((at(off), at(0)), (at(0), at(off))):
+            assert rq.rq_append(bf.h, 0, 0, k, v, 3) == rq.RQ_ERR_INVALID
+            assert rq.rq_append(cache.h, 0, 1, k, v, 3) == rq.RQ_ERR_INVALID
+            assert rq.rq_append_decode_attn(cache.h, 0, 1, k, v, 3, q, out) == rq.RQ_ERR_INVALID
+    assert bf.length(0, 0) == 0 and cache.tail_length(0, 1) == 0
+    space = torch.full((3 * 256 + 8,), 7.0, device="cuda")
+    for qo, oo in ((1, 0), (2, 0), (0, 1), (0, 2)):
+        assert rq.rq_prefill_attn(cache.h, 0, 3, at(qo), 3, space[oo:oo + 768], 0.0) == rq.RQ_ERR_INVALID
+    torch.cuda.synchronize()
+    assert (space == 7.0).all() and (out == 7.0).all()
+    for j in range(3):
+        cache.append(0, j, at(0), at(0))
+    for k, v in ((at(1), at(0)), (at(0), at(2))):
+        assert rq.rq_append(cache.h, 0, 3, k, v, 3) == rq.RQ_ERR_INVALID
+    assert rq.rq_append(cache.h, 0, 3, at(4), at(8), 3) == rq.RQ_OK      # 8 bytes do at the anchor loop
+    k, v = cache.read(0, 3, t0=20, dtype=torch.float32)
+    assert (k - at(4).float()).abs().max() <= 0.4 and (v - at(8).float()).abs().max() <= 0.4
+    cache.check()
+    cache.close()
+    bf.close()
