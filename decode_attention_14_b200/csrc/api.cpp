@@ -919,24 +919,31 @@ bool capturing(cudaStream_t st) {
 }
 
 // Makes *p a device buffer of at least `need` bytes (*have: its size), kept by
-// the cache and grown on demand.  Growing synchronises the device, unless a
-// captured graph may hold the old buffer: that is kept until the cache is
-// destroyed.  While `st` is being captured nothing can be allocated: NOMEM, the
-// capture left valid.
-int grow_buffer(rq_cache *c, void **p, size_t *have, size_t need, cudaStream_t st) {
+// the cache and grown on demand, to twice its size (not beyond `most`, what the
+// largest call needs) or what the call needs: each chunk of a prompt sees more
+// than the one before.  Growing synchronises the device, unless a captured graph
+// may hold the old buffer: that is kept until the cache is destroyed (all of them
+// together less than twice the last).  While `st` is being captured nothing
+// can be allocated: NOMEM, the capture left valid.
+int grow_buffer(rq_cache *c, void **p, size_t *have, size_t need, cudaStream_t st, size_t most = SIZE_MAX) {
     const bool cap = capturing(st);
     if (need > *have) {
         if (cap) return RQ_ERR_NOMEM;
         void *q = nullptr;
+        size_t size = std::max(need, std::min(most, 2 * *have));
         if (*p && !c->captured) {   // freed first, so that both need not fit at once
             if (cudaDeviceSynchronize() != cudaSuccess) return RQ_ERR_CUDA;
             cudaFree(*p);
             *p = nullptr;
             *have = 0;
         }
-        if (cudaMalloc(&q, need) != cudaSuccess) {
+        if (cudaMalloc(&q, size) != cudaSuccess) {
             cudaGetLastError();
-            return RQ_ERR_NOMEM;
+            size = need;
+            if (cudaMalloc(&q, size) != cudaSuccess) {
+                cudaGetLastError();
+                return RQ_ERR_NOMEM;
+            }
         }
         if (*p) {
             try {
@@ -947,7 +954,7 @@ int grow_buffer(rq_cache *c, void **p, size_t *have, size_t need, cudaStream_t s
             }
         }
         *p = q;
-        *have = need;
+        *have = size;
     }
     if (cap && need > 0) c->captured = true;
     return RQ_OK;
@@ -979,7 +986,10 @@ int plan_rebuild(rq_cache *c, const PrefillArgs &a, cudaStream_t st, ReadArgs *r
     const int parts = a.out16 ? 3 : 4;                   // K in two; V in two for fp32 output
     const int heads = (int)std::min<size_t>(a.H, std::max<size_t>(1, kRebuildMax / (head * 2 * parts)));
     const size_t part = head * heads;
-    const int s = grow_buffer(c, (void **)&c->rebuild_ws, &c->rebuild_bytes, part * 2 * parts, st);
+    // what a call for all tokens the cache holds needs, in fp32
+    const size_t full = (size_t)a.B * (c->lay.Tp + a.tail_cap + 143) * kHeadDim * 2 * 4;
+    const size_t most = std::min(full * a.H, std::max(full, kRebuildMax));
+    const int s = grow_buffer(c, (void **)&c->rebuild_ws, &c->rebuild_bytes, part * 2 * parts, st, most);
     if (s != RQ_OK) return s;
     std::memset(r, 0, sizeof(*r));
     for (int kv = 0; kv < 2; kv++) {

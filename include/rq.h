@@ -252,7 +252,7 @@ int rq_decode_attn_bf16(rq_cache *cache, int layer, int loop, const void *q_bf16
  * the n new tokens are the last ones -- committed at an anchor loop, in the
  * tail at the other loops -- and each sees itself and the ones before it.
  * The split partials live in a device buffer the cache allocates on the
- * first call (and grows when a later call needs more:
+ * first call (and grows, to at least twice its size, when a later call needs more:
  * batch * n_tokens * num_q_heads * splits * 132 floats), and the arrival
  * counters of the splits (batch * num_kv_heads *
  * ceil(n_tokens * num_q_heads / num_kv_heads / 64)
@@ -330,10 +330,11 @@ int rq_decode_attn_window(rq_cache *cache, int layer, int loop, const void *q_bf
  * needs more: split partials, and for compressed caches the rebuilt rows:
  * batch * (tokens visible to any of the n, + 143 at most) * 768 bytes a kv head
  * (1024 with fp32 output), for as many kv heads at a time as 4 GiB hold, at
- * least one.  Growing synchronises the device and cannot be done while `stream`
- * is being captured (NOMEM, the capture stays valid): make the first call of a
- * size before.  Buffers that a captured call uses stay until rq_cache_destroy,
- * also when outgrown.  Calls on one cache share them: calls whose work overlaps
+ * least one.  A buffer that is too small grows to at least twice its size.
+ * Growing synchronises the device and cannot be done while `stream` is being
+ * captured (NOMEM, the capture stays valid): make the first call of a size
+ * before.  Buffers that a captured call uses stay until rq_cache_destroy, also
+ * when outgrown.  Calls on one cache share them: calls whose work overlaps
  * (other streams, two replayed graphs) must be ordered by the caller.
  * Errors: INVALID (null or unaligned pointer, n_tokens < 1, index, window < 0,
  * sinks < 0, out_type), STATE (a sequence holds fewer than n_tokens tokens), UNSUPPORTED

@@ -201,3 +201,31 @@ def test_appended_rows_off_their_alignment_are_refused():
     cache.check()
     cache.close()
     bf.close()
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_buffers_of_a_growing_prompt(captured):
+    """A prompt in chunks of 64, each of which sees all before it: the buffers that the cache keeps (after a captured call
+    also those outgrown) take a small multiple of the largest call's, and few calls allocate."""
+    heads, chunk, T = 8, 64, 8192
+    cache = make(heads=heads, Hq=heads, Lg=1, max_tokens=T)
+    k, v, q = (normal(s, 1, chunk, heads, 128).bfloat16() for s in (41, 42, 43))
+    out = torch.empty((1, chunk, heads, 128), device="cuda")
+    torch.cuda.synchronize()
+    free = start = torch.cuda.mem_get_info()[0]
+    steps = 0
+    for t in range(0, T, chunk):
+        cache.append(0, 0, k, v)
+        cache.prefill_window(0, 0, q, 0, out=out)
+        if t == 0 and captured:
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                cache.prefill_window(0, 0, q, 0, out=out)
+        now = torch.cuda.mem_get_info()[0]
+        steps += now != free
+        free = now
+    need = heads * (T + 143) * 1024 + heads * chunk * 256 * 132 * 4     # rebuilt rows, and the most that partials take
+    assert start - free <= 4 * need + (64 << 20), (start - free, need)
+    assert steps <= 24, steps
+    cache.check()
+    cache.close()
