@@ -12,6 +12,10 @@
 
 namespace rq {
 
+// The maximum a windowed call's split leaves beside the sum of its weights: a
+// sum that is NaN counts whatever the maximum of the other logits is.
+__device__ __forceinline__ float split_max(float m, float l) { return l != l ? 0.f : m; }
+
 // The split partials of a row merged into (M, l, o) for element tid:
 // kBatch splits per round of loads (one round for up to kBatch splits), the
 // batch's maximum, the running sums rescaled to it, then the batch folded in
@@ -53,12 +57,14 @@ __device__ __forceinline__ void merge_partials(const float *part, int S, int tid
 // Run by 128 threads (thread `tid` owns element tid of the row).  `sync` is a
 // barrier over exactly those threads; `red` is 4 floats of shared memory.
 // Tail tokens [hole.first, hole.last) are masked; the row goes to out_row, or
-// as BF16 to out16 where that is given.
+// as BF16 to out16 where that is given.  A sum of weights that is NaN (a logit
+// was) makes the row zero, or with nan_shows (the windowed calls) NaN.
 template <int kBatch = 16, typename Sync>
 __device__ __forceinline__ void combine_row(const float *part, int S, const uint16_t *q_row, float scale_log2,
                                             const uint16_t *tail_k, const uint16_t *tail_v, size_t tail_stride,
                                             int n_tail, float *out_row, int tid, float *red, Sync sync,
-                                            TailMask hole = TailMask{0, 0}, uint16_t *out16 = nullptr) {
+                                            TailMask hole = TailMask{0, 0}, uint16_t *out16 = nullptr,
+                                            bool nan_shows = false) {
     const int lane = tid & 31, warp = tid >> 5;
     // q and the first tail token are fetched first, so that their latency
     // overlaps the partials' (L2 loads: the tail rows may have been written
@@ -89,7 +95,7 @@ __device__ __forceinline__ void combine_row(const float *part, int S, const uint
         l = l * c0 + c1;
         M = nm;
     }
-    const float x = (l > 0.f) ? o / l : 0.f;
+    const float x = (nan_shows ? l != 0.f : l > 0.f) ? o / l : 0.f;
     if (out16) out16[tid] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
     else out_row[tid] = x;
 }

@@ -155,8 +155,9 @@ __global__ void __launch_bounds__(128, WIN ? (GK == 1 ? 10 : 7) : 0) decode_bf16
         float *part = a.partials + (((size_t)b * a.Hq + hq0 + gq) * a.splits_max + split) * kPartialStride;
         part[tid] = s_acc[0][gq][tid] + s_acc[1][gq][tid] + s_acc[2][gq][tid] + s_acc[3][gq][tid];
         if (tid == 0) {
-            part[kHeadDim] = M[gq];
-            part[kHeadDim + 1] = s_lsum[0][gq] + s_lsum[1][gq] + s_lsum[2][gq] + s_lsum[3][gq];
+            const float l = s_lsum[0][gq] + s_lsum[1][gq] + s_lsum[2][gq] + s_lsum[3][gq];
+            part[kHeadDim] = WIN ? split_max(M[gq], l) : M[gq];
+            part[kHeadDim + 1] = l;
         }
     }
     if (WIN) {
@@ -176,7 +177,7 @@ __global__ void __launch_bounds__(128, WIN ? (GK == 1 ? 10 : 7) : 0) decode_bf16
             const size_t io = (size_t)b * a.ldq + hq0 + gq;
             combine_row<8>(a.partials + row * a.splits_max * kPartialStride, a.S, a.q + io * kHeadDim, a.scale_log2,
                         nullptr, nullptr, 0, 0, a.out16 ? nullptr : a.out + io * kHeadDim, tid, &s_red[0][0],
-                        BlockSync(), TailMask{0, 0}, a.out16 ? a.out16 + io * kHeadDim : nullptr);
+                        BlockSync(), TailMask{0, 0}, a.out16 ? a.out16 + io * kHeadDim : nullptr, true);
         }
     }
 }
@@ -193,7 +194,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const CombineArgs a) {
                 a.tail_k ? a.tail_k + trow : nullptr, a.tail_v ? a.tail_v + trow : nullptr, (size_t)a.H * kHeadDim,
                 a.n_tail, a.out16 ? nullptr : a.out + io * kHeadDim, tid, s_red, BlockSync(),
                 a.window > 0 ? tail_mask(0, a.n_tail, a.window, a.sinks) : TailMask{0, 0},
-                a.out16 ? a.out16 + io * kHeadDim : nullptr);
+                a.out16 ? a.out16 + io * kHeadDim : nullptr, a.window > 0);
 }
 
 }  // namespace

@@ -1023,7 +1023,7 @@ __global__ void __launch_bounds__(kThreads, GK == 1 ? RQ_DECODE_MIN_CTAS : 3) de
         float *part = a.partials + (((size_t)b * a.Hq + hq0 + gq) * a.splits_max + split) * kPartialStride;
         part[tid] = oA[gq] + oR[gq];
         if (tid == 0) {
-            part[kHeadDim] = M[gq];
+            part[kHeadDim] = WIN ? split_max(M[gq], Lsum[gq]) : M[gq];
             part[kHeadDim + 1] = Lsum[gq];
         }
     }
@@ -1047,7 +1047,7 @@ __global__ void __launch_bounds__(kThreads, GK == 1 ? RQ_DECODE_MIN_CTAS : 3) de
                 combine_row(a.partials + row * a.splits_max * kPartialStride, a.S, a.q + io * kHeadDim, a.scale_log2,
                             tail_k, tail_v, (size_t)a.H * kHeadDim, a.n_tail,
                             a.out16 ? nullptr : a.out + io * kHeadDim, tid, &s_red[0][0], ConsumerSync(),
-                            tail_mask(a.seqT.v[b], a.n_tail, a.window, a.sinks), a.out16 ? a.out16 + io * kHeadDim : nullptr);
+                            tail_mask(a.seqT.v[b], a.n_tail, a.window, a.sinks), a.out16 ? a.out16 + io * kHeadDim : nullptr, true);
             } else {
                 combine_row(a.partials + row * a.splits_max * kPartialStride, a.S, a.q + row * kHeadDim, a.scale_log2,
                             tail_k, tail_v, (size_t)a.H * kHeadDim, a.n_tail, a.out + row * kHeadDim, tid, &s_red[0][0],

@@ -291,8 +291,8 @@ int rq_prefill_attn(rq_cache *cache, int layer, int loop, const void *q_bf16, in
  * tokens, nearly all of them visible: the tokens between the runs are read too);
  * masked tokens do not enter the result, whatever they hold (the value weights'
  * fixed point of a compressed cache is relative to the largest FP8 scale ever
- * written to the stream, masked tokens' among them).  With no token at all the
- * output is zero.  fp32 results are more precise than rq_decode_attn's (31-bit
+ * written to the stream, masked tokens' among them); a visible token whose K or
+ * V is NaN makes the row NaN.  With no token at all the output is zero.  fp32 results are more precise than rq_decode_attn's (31-bit
  * instead of 22-bit value weights); BF16 output is the fp32 result rounded once.
  * RQ_FMT_BF16 with four or more query heads a kv head (and no empty sequence):
  * the arithmetic of rq_prefill_attn_window over such a cache, on the tensor

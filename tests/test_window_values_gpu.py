@@ -229,3 +229,50 @@ def test_buffers_of_a_growing_prompt(captured):
     assert steps <= 24, steps
     cache.check()
     cache.close()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("fmt,Hq", [(rq.RQ_FMT_RESIDUAL, 2), (rq.RQ_FMT_RESIDUAL, 8), (rq.RQ_FMT_BF16, 2), (rq.RQ_FMT_BF16, 8)])
+@pytest.mark.parametrize("what", ["k", "v"])
+def test_a_visible_nan_shows(what, fmt, Hq, dtype):
+    """A NaN in a visible token's K or V makes its kv head's rows NaN, in the single-token call as in a chunk, also where it
+    is the only token seen; the other sequences' and heads' rows are as they were."""
+    cache = make(B=3, heads=2, Hq=Hq, Lg=1, max_tokens=400, fmt=fmt)
+    k, v = (normal(s, 3, 300, 2, 128).bfloat16() for s in (51, 52))
+    (k if what == "k" else v)[1, 260:262, 1] = float("nan")
+    cache.append(0, 0, k, v)
+    cache.truncate_seq(0, 0, 1, 261)
+    kr, vr = cache.read(0, 0, dtype=torch.float32)
+    q = normal(53, 3, 1, Hq, 128).bfloat16()
+    for window in (100, 1, 0):
+        got = cache.decode_window(0, 0, q[:, 0].contiguous(), window, dtype=dtype)
+        assert torch.isnan(got[1, Hq // 2:]).all(), window
+        for b, heads in ((0, slice(0, Hq)), (1, slice(0, Hq // 2)), (2, slice(0, Hq))):
+            P = 261 if b == 1 else 300
+            kb, vb = (x[b:b + 1, :P].nan_to_num(0.0) for x in (kr, vr))
+            ref = reference(kb, vb, q[b:b + 1], window, 0)[0, 0]
+            close(got[b, heads], ref[heads], TOL[dtype])
+    chunk = cache.prefill_window(0, 0, normal(54, 3, 9, Hq, 128).bfloat16(), 100, dtype=dtype)
+    assert torch.isnan(chunk[1, -1, Hq // 2:]).all() and torch.isfinite(chunk[1, :-1]).all() and torch.isfinite(chunk[0]).all()
+    cache.check()
+    cache.close()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+def test_a_nan_of_the_tail_shows(dtype):
+    """The same for tail tokens, with committed ones before them and without."""
+    for T in (0, 90):
+        cache = make(heads=2, Hq=4)
+        for j in range(4 if T else 0):
+            cache.append(0, j, normal(j, 1, T, 2, 128).bfloat16(), normal(9 + j, 1, T, 2, 128).bfloat16())
+        k, v = (normal(s, 1, 6, 2, 128).bfloat16() for s in (55, 56))
+        k[0, 3, 1], v[0, 1, 0, 7] = float("nan"), float("nan")
+        cache.append(0, 1, k, v)
+        q = normal(57, 1, 4, 128).bfloat16()
+        for window, sinks in ((6, 0), (4, 0), (2, 0), (3, 4) if T else (1, 4), (0, 0)):
+            seen = lambda t: window == 0 or t >= 6 - window or T + t < sinks      # noqa: E731
+            got = cache.decode_window(0, 1, q, window, sinks, dtype=dtype)
+            assert torch.isnan(got[0, 2:]).all() == seen(3) and torch.isfinite(got[0, 2:]).all() == (not seen(3)), (T, window)
+            assert torch.isnan(got[0, :2, 7]).all() == seen(1) and torch.isfinite(got[0, :2, :7]).all(), (T, window)
+        cache.check()
+        cache.close()
