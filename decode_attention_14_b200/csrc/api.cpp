@@ -1028,18 +1028,23 @@ int plan_rebuild(rq_cache *c, const PrefillArgs &a, cudaStream_t st, ReadArgs *r
 // New tokens up to which a windowed chunk runs token by token through the decode
 // kernels, which read the visible records once for every token and every two
 // heads (`passes`), instead of rebuilding them for the tensor cores once for all.
-// Compressed caches, one residual, BF16 output, 4 x 16 heads, us for 1 / 2 / 3 / 4
-// tokens: 8192 visible tokens 38 / 77 / 115 / 153 against 174, 1024: 11 / 24 / 37 /
-// 50 against 36, 128: 8 / 17 / 25 / 33 against 14 / 18 / 18 / 18; heads in groups
-// of 4, 8 kv heads, 8192: 24 against 31, 1024: 13.6 against 13.1; groups of 8, 4 kv
-// heads, 16384: 38 against 33.  fp32 output leaves more room (250 / 53 / 17, 40 /
-// 15.2, 43).  BF16 caches: one token, 4 x 16 heads, 1024 visible, 12.2 against
+// Compressed caches, us for one token alone against a chunk of up to 8 to BF16 /
+// fp32 output:
+//   4 x 16 heads, residual loop: 8192 visible tokens 39 against 203 / 250, 4096: 24
+//   against 109 / 136, 1024: 11 against 37 / 49, 256: 8.5 against 16 / 18; at the
+//   anchor loop, 8192: 21 against 161 / 220;
+//   2 heads per kv head, 16 kv heads, residual, 8192: 72 against 203 / 250;
+//   4 per kv head, 8 kv heads, 8192: residual 71 against 109 / 137, anchor 35
+//   against 86 / 117; 256: 12 against 13 / 14;
+//   8 per kv head, 4 kv heads, 16384: residual 141 against 115 / 138, anchor 63
+//   against 92 / 120; 1024: anchor 11 against 17 / 18.
+// BF16 caches: one token, 4 x 16 heads, 1024 visible, 12.2 against
 // 16.4, 128: 7.0 against 8.5, 8192: 49 against 47; groups of 4 (one pass over K and V
 // for the four on the tensor cores, two in the decode kernel), 8 kv heads, 8192: 28
 // against 13, 128: 8.1 against 8.2; groups of 8, 4 kv heads, 16384: 37 against 15 --
 // so there rq_decode_attn_window goes to the chunk's kernel too (fp32 output: error
 // 1 to 3e-6 relative, BF16 pairs of weights, instead of 4e-7, for half the time).
-int few_rows(const rq_cache *c, const SeqLens &lens, int n_tail, const WindowSpec &win) {
+int few_rows(const rq_cache *c, const SeqLens &lens, int n_tail, bool anchor, const WindowSpec &win) {
     const rq_config &cfg = c->lay.cfg;
     const int G = cfg.num_q_heads / cfg.num_kv_heads, passes = G > 2 ? G / 2 : 1;
     if (cfg.format == RQ_FMT_BF16) return passes == 1 ? 1 : 0;
@@ -1047,8 +1052,9 @@ int few_rows(const rq_cache *c, const SeqLens &lens, int n_tail, const WindowSpe
     for (int b = 0; b < cfg.batch; b++)
         seen += std::min((long long)lens.v[b] + n_tail, (long long)win.window + win.sinks);
     seen *= cfg.num_kv_heads;
-    const int most = seen >= 1 << 18 ? 4 : seen >= 1 << 16 ? 2 : 1;
-    return std::max(passes <= 2 ? 1 : 0, most / passes);
+    int most = seen >= 1 << 18 ? 4 : seen >= 1 << 16 ? 2 : 1;
+    if (G == 1 && win.out_type == RQ_OUT_FP32 && most > 1) most++;   // the chunk's second parts take longer
+    return std::max(passes <= 2 || anchor ? 1 : 0, most / (anchor ? passes : passes * passes));
 }
 
 // win == nullptr: rq_prefill_attn
@@ -1089,7 +1095,7 @@ int prefill_common(rq_cache *c, int layer, int loop, const void *q, int n, void 
     // the n new tokens must be the most recent of every sequence
     for (int b = 0; b < cfg.batch; b++)
         if (a.seqT.v[b] + a.n_tail < n) return RQ_ERR_STATE;
-    if (win && n <= few_rows(c, a.seqT, a.n_tail, *win)) {
+    if (win && n <= few_rows(c, a.seqT, a.n_tail, !a.r_codes[0], *win)) {
         WindowSpec w = *win;
         w.rows = n;
         for (w.row = 0; w.row < n; w.row++) {

@@ -318,8 +318,8 @@ int rq_decode_attn_window(rq_cache *cache, int layer, int loop, const void *q_bf
  *   window, sinks, softmax_scale: as for rq_decode_attn_window.
  * A masked token does not enter a row, whatever it holds; a row that sees a V
  * that is not finite is not finite either (from the tensor cores NaN as a whole).
- * Arithmetic: one to four tokens, where that is less work, run one by one as
- * rq_decode_attn_window does (n_tokens, the heads per kv head and the number of
+ * Arithmetic: one to five tokens, where that is less work, run one by one as
+ * rq_decode_attn_window does (n_tokens, the heads per kv head, the loop, out_type and the number of
  * visible tokens decide).  Else: products on the tensor cores with fp32 sums.  BF16 caches: exact
  * products of q and K; the weights are BF16 for BF16 output (half a step, 2^-9,
  * of each weight beside the output's own rounding), two BF16 parts (2^-18) for

@@ -8,7 +8,9 @@ Tolerances, of each output row's norm.  fp32 output: a row and its weight are
 two BF16 numbers each, off by at most half a step of the second, 2^-18: at
 random signs over 128 products and over the tokens that is a few 1e-6 of the
 logits and of the row, and the tensor cores' sums leave up to 3.5e-6: 2e-5.
-BF16 output: half a step, 2^-9 of each element, and 2^-9 of each weight: 2^-8.
+BF16 output: half a step, 2^-9, of each element, of each weight and of each V; a
+rounding's root mean square is 2^-9 / sqrt(3) at most, so all three, at random
+signs, make 2^-9: 2^-8.
 """
 import numpy as np
 import pytest
@@ -276,3 +278,27 @@ def test_a_nan_of_the_tail_shows(dtype):
             assert torch.isnan(got[0, :2, 7]).all() == seen(1) and torch.isfinite(got[0, :2, :7]).all(), (T, window)
         cache.check()
         cache.close()
+
+
+@pytest.mark.parametrize("Hkv,Hq,T", [(32, 32, 4200), (16, 16, 2100), (32, 128, 2100), (16, 128, 4200)])
+def test_chunks_on_either_side_of_the_rule_for_few_tokens(Hkv, Hq, T):
+    """One to seven tokens over many, one head per kv head and groups, an anchor and a residual loop, both output types: the
+    rows agree with the formula wherever the rule sends them.
+
+    BF16 output of a chunk has three roundings of at most half a step, 2^-9: the output's, d_o o, and in the sum those of each
+    weight and of each V, sum_t p_t v_t (d_p + d_v).  Values here are independent with mean zero, so the norm of the sum is
+    that of its terms, |o|^2 = sum_t p_t^2 |v_t|^2, and |sum_t p_t v_t d| <= 2^-9 |o| for roundings of either kind at random
+    signs (their root mean square is smaller by sqrt(3) at least).  Together 3 2^-9, against a most likely 2.9e-3 = 1.5 2^-9."""
+    tol = {torch.float32: TOL[torch.float32], torch.bfloat16: 3 * 2.0 ** -9}
+    cache = make(B=2, heads=Hkv, Hq=Hq, Lg=2, max_tokens=T, tail=T)
+    for j in range(2):
+        cache.append(0, j, normal(70 + j, 2, T, Hkv, 128).bfloat16(), normal(72 + j, 2, T, Hkv, 128).bfloat16())
+    for loop in (0, 1):
+        kr, vr = cache.read(0, loop, dtype=torch.float32)
+        for n in (1, 2, 3, 5, 6, 7):
+            q = normal(80 + n, 2, n, Hq, 128).bfloat16()
+            ref = torch.cat([reference(kr[b:b + 1], vr[b:b + 1], q[b:b + 1], 0, 0) for b in range(2)])
+            for dtype in TOL:
+                close(cache.prefill_window(0, loop, q, 0, dtype=dtype), ref, tol[dtype])
+    cache.check()
+    cache.close()
