@@ -204,6 +204,21 @@ def _stream(stream) -> int:
     return int(getattr(stream, "cuda_stream", stream))
 
 
+def _new(make, shape, dtype, device, stream):
+    """A new output of a call on `stream`, by `make` (torch.empty or torch.zeros): memory of that stream's, filled in its
+    order, and not given out again before what the current stream does with it has run."""
+    import torch
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        t = make(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _check_dev(t, dtype_name: str, shape, what: str):
     import torch
     if not (t.is_cuda and t.is_contiguous()):
@@ -402,7 +417,7 @@ class Cache:
         import torch
         _check_dev(q, "bfloat16", (self.B, self.Hq, HEAD_DIM), "q")
         if out is None:
-            out = torch.empty((self.B, self.Hq, HEAD_DIM), dtype=torch.float32, device=q.device)
+            out = _new(torch.empty, (self.B, self.Hq, HEAD_DIM), torch.float32, q.device, stream)
         _check_dev(out, "float32", (self.B, self.Hq, HEAD_DIM), "out")
         fn = rq_decode_attn_bf16 if bf16 else rq_decode_attn
         _ok(fn(self.h, layer, loop, q, out, scale, stream), fn.__name__)
@@ -414,18 +429,18 @@ class Cache:
         format; q [batch][num_q_heads][128] bf16 -> `dtype` (float32 unless given, or bfloat16) of the same shape."""
         shape = (self.B, self.Hq, HEAD_DIM)
         _check_dev(q, "bfloat16", shape, "q")
-        out = self._window_out(out, dtype, shape, q)
+        out = self._window_out(out, dtype, shape, q, stream)
         self._on_device(q, out)
         _ok(rq_decode_attn_window(self.h, layer, loop, q, out, _out_type(out.dtype), scale, window, sinks, stream),
             "rq_decode_attn_window")
         return out
 
     @staticmethod
-    def _window_out(out, dtype, shape, q):
+    def _window_out(out, dtype, shape, q, stream):
         import torch
         _check_aligned(q, "q")
         if out is None:
-            return torch.empty(shape, dtype=dtype or torch.float32, device=q.device)
+            return _new(torch.empty, shape, dtype or torch.float32, q.device, stream)
         if dtype is not None and out.dtype != dtype:
             raise ValueError(f"out is {out.dtype}, not {dtype}")
         _check_dev(out, "bfloat16" if out.dtype == torch.bfloat16 else "float32", shape, "out")
@@ -439,7 +454,7 @@ class Cache:
         n = q.shape[1]
         _check_dev(q, "bfloat16", (self.B, n, self.Hq, HEAD_DIM), "q")
         if out is None:
-            out = torch.empty((self.B, n, self.Hq, HEAD_DIM), dtype=torch.float32, device=q.device)
+            out = _new(torch.empty, (self.B, n, self.Hq, HEAD_DIM), torch.float32, q.device, stream)
         _check_dev(out, "float32", (self.B, n, self.Hq, HEAD_DIM), "out")
         _ok(rq_prefill_attn(self.h, layer, loop, q, n, out, scale, stream), "rq_prefill_attn")
         return out
@@ -452,7 +467,7 @@ class Cache:
         n = q.shape[1]
         shape = (self.B, n, self.Hq, HEAD_DIM)
         _check_dev(q, "bfloat16", shape, "q")
-        out = self._window_out(out, dtype, shape, q)
+        out = self._window_out(out, dtype, shape, q, stream)
         self._on_device(q, out)
         _ok(rq_prefill_attn_window(self.h, layer, loop, q, n, out, _out_type(out.dtype), scale, window, sinks, stream),
             "rq_prefill_attn_window")
@@ -467,7 +482,7 @@ class Cache:
         _check_dev(v, "bfloat16", shape, "v")
         _check_dev(q, "bfloat16", (self.B, self.Hq, HEAD_DIM), "q")
         if out is None:
-            out = torch.empty((self.B, self.Hq, HEAD_DIM), dtype=torch.float32, device=q.device)
+            out = _new(torch.empty, (self.B, self.Hq, HEAD_DIM), torch.float32, q.device, stream)
         _check_dev(out, "float32", (self.B, self.Hq, HEAD_DIM), "out")
         _ok(rq_append_decode_attn(self.h, layer, loop, k, v, n, q, out, scale, stream), "rq_append_decode_attn")
         return out
@@ -494,7 +509,7 @@ class Cache:
             raise ValueError(f"no token from {t0} on")
         if k is None:
             shape = (self.B, n, self.H, HEAD_DIM)
-            k, v = (torch.zeros(shape, dtype=dtype or torch.bfloat16, device=self.device) for _ in range(2))
+            k, v = (_new(torch.zeros, shape, dtype or torch.bfloat16, self.device, stream) for _ in range(2))
         for x, what in ((k, "k"), (v, "v")):
             _check_rows(x, (self.B, n, self.H, HEAD_DIM), what)
         self._on_device(k, v)

@@ -302,3 +302,29 @@ def test_chunks_on_either_side_of_the_rule_for_few_tokens(Hkv, Hq, T):
                 close(cache.prefill_window(0, loop, q, 0, dtype=dtype), ref, tol[dtype])
     cache.check()
     cache.close()
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_new_outputs_on_another_stream_than_the_current_one(handle):
+    """The current stream is busy for some milliseconds: rows that a call on a side stream writes into its own new tensors
+    are not overwritten by their zeroing, and new tensors do not take memory that the current stream still works on."""
+    cache = make(B=2, heads=2, Hq=4, Lg=1)
+    cache.append(0, 0, normal(91, 2, 300, 2, 128).bfloat16(), normal(92, 2, 300, 2, 128).bfloat16())
+    q1, qn = normal(93, 2, 4, 128).bfloat16(), normal(94, 2, 30, 4, 128).bfloat16()
+    calls = [lambda **kw: cache.read(0, 0, **kw)[0], lambda **kw: cache.read(0, 0, dtype=torch.float32, **kw)[1],
+             lambda **kw: cache.decode_window(0, 0, q1, 50, **kw), lambda **kw: cache.prefill_window(0, 0, qn, 50, **kw),
+             lambda **kw: cache.decode(0, 0, q1, **kw), lambda **kw: cache.prefill(0, 0, qn, **kw)]
+    want = [call() for call in calls]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for call, w in zip(calls, want):
+        busy = torch.full(w.shape, 3.0, dtype=w.dtype, device="cuda")
+        torch.cuda._sleep(20_000_000)                       # about 10 ms
+        kept = busy * 2.0                                   # still to run when busy's memory is free again
+        del busy
+        got = call(stream=side.cuda_stream if handle else side)
+        torch.cuda.synchronize()
+        assert torch.equal(got, w) and (kept == 6.0).all()
+        del got, kept
+    cache.check()
+    cache.close()
