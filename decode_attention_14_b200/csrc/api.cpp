@@ -1022,6 +1022,7 @@ int plan_rebuild(rq_cache *c, const PrefillArgs &a, cudaStream_t st, ReadArgs *r
     r->window = a.window;
     r->sinks = a.sinks;
     r->nonfinite = nonfinite_ptr(c);
+    r->sms = c->sms;
     return RQ_OK;
 }
 
@@ -1341,6 +1342,7 @@ int rq_cache_read(rq_cache *c, int layer, int loop, int t0, int n, int out_type,
     a.t0 = t0;
     a.tail_cap = L.tail_cap;
     a.Tp = L.Tp;
+    a.sms = c->sms;
     a.g = cfg.group_size;
     a.rotate = cfg.rotate;
     a.pg = pages_of(c);

@@ -76,9 +76,9 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 // set-up and overlap, as long as four rounds of the 16 warps an SM holds remain
 // to even out the end: at 8k b4 (residual) 99 / 104 / 119 us with 4 / 2 / 1, at
 // 15 000 tiles 24.4 / 21.1 / 21.2 us.
-inline int warp_tiles(long long tiles) {
+inline int warp_tiles(long long tiles, int sms) {
     int per = kTiles;
-    while (per > 1 && tiles < 148LL * 16 * 4 * per) per /= 2;
+    while (per > 1 && tiles < (long long)sms * 16 * 4 * per) per /= 2;
     return per;
 }
 

@@ -24,7 +24,8 @@ struct ReadArgs {
     SeqLens seqT;                      // committed tokens of each sequence
     Pages pg;
     int B, H, t0, n, n_tail, tail_cap, Tp;
-    int tiles;                         // 16-token tiles per warp (set by launch_read)
+    int sms;                           // of the device
+    int tiles;                         // 16-token tiles per warp (set by the launches)
     int g;
     int rotate;
     uint32_t sigma[4];

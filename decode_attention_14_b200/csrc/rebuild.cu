@@ -25,7 +25,7 @@ cudaError_t launch_bits(const ReadArgs &a, unsigned blocks, cudaStream_t st) {
 cudaError_t launch_rebuild(const ReadArgs &args, int ba, int br, cudaStream_t st) {
     ReadArgs a = args;
     const long long units = 2LL * a.B * a.H, nt = a.pair_rows / kRecs;
-    a.tiles = warp_tiles(units * nt);
+    a.tiles = warp_tiles(units * nt, a.sms);
     const int per = a.tiles * kWarps;
     const long long blocks = units * ((nt + per - 1) / per);
     if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
