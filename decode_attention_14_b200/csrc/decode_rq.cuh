@@ -60,8 +60,9 @@
 // P - 1 (P = committed + tail tokens) sees the positions p >= P - window and
 // p < sinks: at most two runs of whole 64-token tiles, [0, sinks) and the
 // window's tiles, each dealt over splits of its own, so that a CTA's tokens
-// stay one run.  Tokens of the first window tile before the window are masked
-// (weight zero whatever their records hold).  The V weights have 31 bits of
+// stay one run.  Tokens of the first window tile before the window, or, where the
+// runs take more splits than there are and are dealt out as one, whole tiles
+// between them, are masked (weight zero whatever their records hold).  The V weights have 31 bits of
 // fixed point instead of 22: with the high halves then needed for most tokens
 // an 8k b4 call takes 5% longer, and the relative L2 error of the output falls
 // from 2e-4 to 1.5e-6.  The bound is the stream's largest V scale, masked

@@ -15,8 +15,10 @@
 //   O += P V    8 MMAs of 128x128x16 with P from tensor memory, for each of P's
 //               PP BF16 parts: one for BF16 output (half a step, 2^-9 of each
 //               weight, is as small as the output's own rounding), a high and
-//               a low one for fp32 output (2^-18; a third one did not lower the
-//               3e-6 that the tensor cores' sums leave)
+//               a low one for fp32 output (2^-18; a third one did not lower what
+//               the tensor cores' sums leave: they are cut off, not rounded,
+//               which makes a row smaller by 2e-9 of itself for every token that
+//               its split sums: 3e-6 for 1500, 2e-5 for 8192)
 // P overwrites S in tensor memory; O is beside it (128 columns each).  Two S
 // buffers keep the tensor cores and the softmax busy at once: with QT = 2 one
 // per row tile -- one tile's MMAs run while the other's softmax does, and both

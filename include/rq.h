@@ -318,6 +318,10 @@ int rq_decode_attn_window(rq_cache *cache, int layer, int loop, const void *q_bf
  *   window, sinks, softmax_scale: as for rq_decode_attn_window.
  * A masked token does not enter a row, whatever it holds; a row that sees a V
  * that is not finite is not finite either (from the tensor cores NaN as a whole).
+ * (Once a V that is not finite was stored in an RQ_FMT_BF16 cache, or seen by a
+ * chunk of a compressed one, every later call of several tokens on that cache
+ * looks all V over and takes up to 2.3 times as long; truncation does not end
+ * that, as the rows past a sequence's end keep what they held.)
  * Arithmetic: one to five tokens, where that is less work, run one by one as
  * rq_decode_attn_window does (n_tokens, the heads per kv head, the loop, out_type and the number of
  * visible tokens decide).  Else: products on the tensor cores with fp32 sums.  BF16 caches: exact
@@ -325,7 +329,11 @@ int rq_decode_attn_window(rq_cache *cache, int layer, int loop, const void *q_bf
  * of each weight beside the output's own rounding), two BF16 parts (2^-18) for
  * fp32 output.  Compressed caches: the same with the visible rows rebuilt in two
  * BF16 parts (2^-18), V in one for BF16 output (2^-9).  All of these are relative
- * to the number itself, whatever its size.
+ * to the number itself, whatever its size.  The tensor cores cut their fp32 sums
+ * off where they do not fit: a row comes out smaller by 2e-9 of itself for every
+ * token summed in one split (measured; 2e-5 for a prompt of 8192 tokens, 9e-5
+ * where a split sums 32768), far below the rounding of BF16 output, but above
+ * all else in an fp32 row of many tokens.
  * Buffers the cache allocates on the first call and grows when a later call
  * needs more: split partials, and for compressed caches the rebuilt rows:
  * batch * (tokens visible to any of the n, + 143 at most) * 768 bytes a kv head
