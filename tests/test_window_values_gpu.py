@@ -328,3 +328,24 @@ def test_new_outputs_on_another_stream_than_the_current_one(handle):
         del got, kept
     cache.check()
     cache.close()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+def test_a_chunk_whose_heads_go_in_groups(dtype):
+    """More rebuilt rows than 4 GiB hold, and more tokens than run one by one: the last token's rows of every head against
+    the single-token call (whose own error is 1e-6).
+
+    The tensor cores cut their sums off: 24 accumulations per 128 tokens (three products of 8 steps), each by less than 2^-23
+    of the sum.  40 row blocks are cut into 4 splits or more, of 40 000 tokens: 24 * 313 * 2^-23 = 9e-4, so 1e-3 for fp32
+    output (2.4e-5 is what they come to).  BF16 output: three roundings of half a step at random signs beside it."""
+    B, Hk, T, n = 8, 5, 160000, 7
+    cache = make(B=B, heads=Hk, Hq=Hk, Lg=1, max_tokens=T)
+    for t in range(0, T, 20000):
+        cache.append(0, 0, normal(t, B, 20000, Hk, 128).bfloat16(), normal(t + 1, B, 20000, Hk, 128).bfloat16())
+    q = normal(95, B, n, Hk, 128).bfloat16()
+    ref = cache.decode_window(0, 0, q[:, -1].contiguous(), 0).double()
+    got = cache.prefill_window(0, 0, q, 0, dtype=dtype)
+    assert torch.isfinite(got).all()
+    close(got[:, -1], ref, 1e-3 + (3 * 2.0 ** -9 if dtype == torch.bfloat16 else 0.0))
+    cache.check()
+    cache.close()
