@@ -1031,14 +1031,14 @@ int plan_rebuild(rq_cache *c, const PrefillArgs &a, cudaStream_t st, ReadArgs *r
 // heads (`passes`), instead of rebuilding them for the tensor cores once for all.
 // Compressed caches, us for one token alone against a chunk of up to 8 to BF16 /
 // fp32 output:
-//   4 x 16 heads, residual loop: 8192 visible tokens 39 against 203 / 250, 4096: 24
-//   against 109 / 136, 1024: 11 against 37 / 49, 256: 8.5 against 16 / 18; at the
-//   anchor loop, 8192: 21 against 161 / 220;
-//   2 heads per kv head, 16 kv heads, residual, 8192: 72 against 203 / 250;
-//   4 per kv head, 8 kv heads, 8192: residual 71 against 109 / 137, anchor 35
-//   against 86 / 117; 256: 12 against 13 / 14;
-//   8 per kv head, 4 kv heads, 16384: residual 141 against 115 / 138, anchor 63
-//   against 92 / 120; 1024: anchor 11 against 17 / 18.
+//   4 x 16 heads, residual loop: 8192 visible tokens 39 against 209 / 250, 4096: 24
+//   against 112 / 137, 1024: 11 against 39 / 49, 256: 8.5 against 17 / 18; at the
+//   anchor loop, 8192: 21 against 162 / 220;
+//   2 heads per kv head, 16 kv heads, residual, 8192: 72 against 207 / 251;
+//   4 per kv head, 8 kv heads, 8192: residual 71 against 113 / 137, anchor 35
+//   against 89 / 118; 256: 12 against 14 / 14;
+//   8 per kv head, 4 kv heads, 16384: residual 141 against 117 / 139, anchor 63
+//   against 94 / 120; 1024: anchor 11 against 17 / 18.
 // BF16 caches: one token, 4 x 16 heads, 1024 visible, 12.2 against
 // 16.4, 128: 7.0 against 8.5, 8192: 49 against 47; groups of 4 (one pass over K and V
 // for the four on the tensor cores, two in the decode kernel), 8 kv heads, 8192: 28

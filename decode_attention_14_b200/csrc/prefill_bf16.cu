@@ -41,14 +41,17 @@
 //
 // RB: the same over a compressed cache.  A first launch (rebuild.cu) writes the
 // tokens that the chunk sees, committed and tail, into a workspace, once for all
-// the chunk's rows, as pairs of BF16 numbers: S = Q (Khi + Klo)^T and, for fp32
-// output, O += (Phi + Plo) Vhi + Phi Vlo; for BF16 output one part of V and of P.
-// What is left out of a number is relative to it (2^-18 of a pair, 2^-9 of one),
-// whatever its size: FP16 operands would be faster (11 bits in one part: 37, 38
-// and 54 us for the cases below instead of 41, 41 and 63), but under any one scale
-// small values, and weights below 2^-25 of the largest, would be lost.  (V in
-// pairs for BF16 output too: 45, 53 and 70 us, the rows' relative error 2.1 to
-// 2.2e-3 instead of 2.2 to 2.7e-3; the output's own rounding makes 1.65e-3.)
+// the chunk's rows, as BF16 numbers: K and V as pairs for fp32 output, V as one
+// number (2^-9, as small as the output's own rounding) for BF16 output:
+//   S = Q (Khi + Klo)^T,  O += (Phi + Plo) Vhi + Phi Vlo.
+// What is left out of a number is relative to it, whatever its size.  FP16
+// operands would be faster (11 bits in one part each: 37, 38 and 54 us for the
+// cases below), but under any one scale small values, and weights below 2^-25 of
+// the largest, would be lost.  BF16 output with one part of P too: 39, 40 and 60
+// us, relative error of the rows 2.2 to 2.7e-3 instead of 1.7 to 2.4e-3 (1.65e-3
+// is the output's rounding); with one of P and two of V: 45, 54 and 70 us.  (P's
+// high part is then cut off rather than rounded, which takes fewer operations: 41
+// instead of 42 us for the first case.)
 //
 // What bounds it: a full chunk is bound by the softmax between the two products
 // (one exponential and about six other operations per logit in a thread per
@@ -58,7 +61,7 @@
 // 511 tokens in two sequences of 4 kv heads of 4, window 1024 (8.6 GFLOP), 30 us.
 // Over compressed caches (all launches, BF16 output): 16 tokens of 4 x 16 heads,
 // window 1024, 41 us; 500 tokens in two sequences of 4 kv heads of 4 heads, window
-// 2000, 41 us; 2048 tokens of 16 heads, window 1024, 63 us.
+// 2000, 48 us; 2048 tokens of 16 heads, window 1024, 70 us.
 //
 // A V row that only some rows see may hold NaN or infinities, which 0 * NaN
 // would carry into the other rows.  The store kernel notes in the arena when it
@@ -204,7 +207,7 @@ struct Runs {
     }
 };
 
-template <int QT, int PP, bool RB>
+template <int QT, int PP, int VP, bool RB>
 __global__ void __launch_bounds__(Cfg<QT>::THREADS, 1)
     prefill_bf16_kernel(const __grid_constant__ Maps maps, const Bf16Args a) {
     using C = Cfg<QT>;
@@ -232,7 +235,7 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, 1)
     const int j0 = (int)((long long)split * runs.tiles / a.S), j1 = (int)((long long)(split + 1) * runs.tiles / a.S);
     const int nt = j1 - j0;
     // stages of tile j of the split: K in KP parts, V in VP
-    constexpr int KP = RB ? 2 : 1, VP = RB ? PP : 1;
+    constexpr int KP = RB ? 2 : 1;
     // S buffer of row tile q's token tile j, and the parity of its phase then
     auto sbuf = [](int q, int j) { return QT == 2 ? q : j & 1; };
     auto sphase = [](int j) { return QT == 2 ? j & 1 : (j >> 1) & 1; };
@@ -479,7 +482,7 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, 1)
                 }
                 l *= f;
                 const float off = m_used == -CUDART_INF_F ? 0.f : -m_used;
-                const F2 sc2 = pack2(scale_log2, scale_log2), off2 = pack2(off, off);
+                const F2 sc2 = pack2(scale_log2, scale_log2), off2 = pack2(off, off), neg1 = pack2(-1.f, -1.f);
                 F2 sum[4];
 #pragma unroll
                 for (int k = 0; k < 4; k++) sum[k] = pack2(0.f, 0.f);
@@ -494,9 +497,18 @@ __global__ void __launch_bounds__(Cfg<QT>::THREADS, 1)
                         p0 = ex2f(p0);
                         p1 = ex2f(p1);
                         sum[k & 3] = add2(sum[k & 3], pack2(p0, p1));
-                        hi[k] = pack_bf16(p0, p1);
-                        if (PP > 1)
-                            low[k] = pack_bf16(p0 - __uint_as_float(hi[k] << 16), p1 - __uint_as_float(hi[k] & 0xFFFF0000u));
+                        const uint32_t b0 = __float_as_uint(p0), b1 = __float_as_uint(p1);
+                        if (RB && VP == 1) {   // BF16 output: the high part cut off, what is left rounded (2^-16)
+                            hi[k] = __byte_perm(b0, b1, 0x7632);
+                            float r0, r1;
+                            unpack2(fma2(pack2(__uint_as_float(b0 & 0xFFFF0000u), __uint_as_float(b1 & 0xFFFF0000u)), neg1,
+                                         pack2(p0, p1)), r0, r1);
+                            low[k] = pack_bf16(r0, r1);
+                        } else {
+                            hi[k] = pack_bf16(p0, p1);
+                            if (PP > 1)
+                                low[k] = pack_bf16(p0 - __uint_as_float(hi[k] << 16), p1 - __uint_as_float(hi[k] & 0xFFFF0000u));
+                        }
                     }
                     __syncwarp();
                     st32(tS + 32 * c, hi);
@@ -665,24 +677,24 @@ cudaError_t launch_overlapped(void (*f)(P...), dim3 grid, int threads, int smem,
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int QT, int PP, bool RB>
+template <int QT, int PP, int VP, bool RB>
 cudaError_t launch_t(const Maps &m, const Bf16Args &a, cudaStream_t st) {
     static bool done[kMaxDevices];
     cudaError_t e = once_per_device(done, [] {
-        return cudaFuncSetAttribute(prefill_bf16_kernel<QT, PP, RB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(prefill_bf16_kernel<QT, PP, VP, RB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     Cfg<QT>::SMEM);
     });
     if (e != cudaSuccess) return e;
-    return launch_overlapped(prefill_bf16_kernel<QT, PP, RB>, dim3(a.S, a.heads, a.B * a.nqb), Cfg<QT>::THREADS,
+    return launch_overlapped(prefill_bf16_kernel<QT, PP, VP, RB>, dim3(a.S, a.heads, a.B * a.nqb), Cfg<QT>::THREADS,
                              Cfg<QT>::SMEM, RB, st, m, a);
 }
 cudaError_t launch_plain(int qt, const Maps &m, const Bf16Args &a, cudaStream_t st) {
-    if (qt == 1) return a.out16 ? launch_t<1, 1, false>(m, a, st) : launch_t<1, 2, false>(m, a, st);
-    return a.out16 ? launch_t<2, 1, false>(m, a, st) : launch_t<2, 2, false>(m, a, st);
+    if (qt == 1) return a.out16 ? launch_t<1, 1, 1, false>(m, a, st) : launch_t<1, 2, 1, false>(m, a, st);
+    return a.out16 ? launch_t<2, 1, 1, false>(m, a, st) : launch_t<2, 2, 1, false>(m, a, st);
 }
 cudaError_t launch_rebuilt(int qt, const Maps &m, const Bf16Args &a, cudaStream_t st) {
-    if (qt == 1) return a.out16 ? launch_t<1, 1, true>(m, a, st) : launch_t<1, 2, true>(m, a, st);
-    return a.out16 ? launch_t<2, 1, true>(m, a, st) : launch_t<2, 2, true>(m, a, st);
+    if (qt == 1) return a.out16 ? launch_t<1, 2, 1, true>(m, a, st) : launch_t<1, 2, 2, true>(m, a, st);
+    return a.out16 ? launch_t<2, 2, 1, true>(m, a, st) : launch_t<2, 2, 2, true>(m, a, st);
 }
 
 // How a call is cut: QT row tiles per CTA and S splits.  The time of the launch

@@ -327,9 +327,9 @@ int rq_decode_attn_window(rq_cache *cache, int layer, int loop, const void *q_bf
  * visible tokens decide).  Else: products on the tensor cores with fp32 sums.  BF16 caches: exact
  * products of q and K; the weights are BF16 for BF16 output (half a step, 2^-9,
  * of each weight beside the output's own rounding), two BF16 parts (2^-18) for
- * fp32 output.  Compressed caches: the same with the visible rows rebuilt in two
- * BF16 parts (2^-18), V in one for BF16 output (2^-9).  All of these are relative
- * to the number itself, whatever its size.  The tensor cores cut their fp32 sums
+ * fp32 output.  Compressed caches: weights and visible rows in two BF16 parts
+ * (2^-18), for BF16 output weights to 2^-16 and V in one part (2^-9).  All of these are relative to the
+ * number itself, whatever its size.  The tensor cores cut their fp32 sums
  * off where they do not fit: a row comes out smaller by 2e-9 of itself for every
  * token summed in one split (measured; 2e-5 for a prompt of 8192 tokens, 9e-5
  * where a split sums 32768), far below the rounding of BF16 output, but above
