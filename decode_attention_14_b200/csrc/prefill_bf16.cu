@@ -53,15 +53,15 @@
 // high part is then cut off rather than rounded, which takes fewer operations: 41
 // instead of 42 us for the first case.)
 //
-// What bounds it: a full chunk is bound by the softmax between the two products
-// (one exponential and about six other operations per logit in a thread per
-// row), not by the MMAs: 8192 causal tokens, 16 heads, 308 us = 892 TFLOP/s,
-// tensor pipe 36% and special-function pipe 37% busy in a 4096-token run.  Few
-// rows over a short window are bound by launches and the pipeline's filling:
-// 511 tokens in two sequences of 4 kv heads of 4, window 1024 (8.6 GFLOP), 30 us.
+// What bounds it: the chain of a tile -- logits, maximum, exponentials, P handed
+// over -- in a thread per row, a warp or two per scheduler; no unit is busy: 8192
+// causal tokens, 16 heads, 313 us = 878 TFLOP/s, tensor pipe 36%, special-function
+// pipe 37%, issue slots 26% in a 4096-token run.  Few rows over a short window
+// also pay for launches and the pipeline's filling: 511 tokens in two sequences of
+// 4 kv heads of 4, window 1024 (8.6 GFLOP), fp32 output, 30 us (tensor pipe 27%).
 // Over compressed caches (all launches, BF16 output): 16 tokens of 4 x 16 heads,
 // window 1024, 41 us; 500 tokens in two sequences of 4 kv heads of 4 heads, window
-// 2000, 48 us; 2048 tokens of 16 heads, window 1024, 70 us.
+// 2000, 48 us; 2048 tokens of 16 heads, window 1024, 70 us (tensor pipe 44%).
 //
 // A V row that only some rows see may hold NaN or infinities, which 0 * NaN
 // would carry into the other rows.  The store kernel notes in the arena when it

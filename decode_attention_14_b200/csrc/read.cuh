@@ -31,9 +31,9 @@
 // asynchronous copies; rows are padded by 16 bytes so that no read of eight
 // records conflicts.
 //
-// What bounds it: instruction issue.  A tile of 16 records with one residual
-// takes about 1100 warp instructions, and an issue slot is used in 66% of the
-// cycles: 4 x 16 heads x 8192 tokens (residual, BF16 out, 405 MB read and
+// What bounds it: instructions, and latency that 16 warps an SM do not hide.  A
+// tile of 16 records with one residual takes about 1100 warp instructions, and an
+// issue slot is used in 66% of the cycles: 4 x 16 heads x 8192 tokens (residual, BF16 out, 405 MB read and
 // written) 98.8 us = 4.1 TB/s, 63% of a plain copy; an anchor group alone to
 // fp32, 13 000 paged tokens x 8 heads (123 MB), 21.1 us = 5.8 TB/s, 89%.
 //

@@ -2,8 +2,9 @@
 // compressed cache as BF16 pairs in a workspace (the first launch of
 // rq_prefill_attn_window): the kOutPair instantiations of read.cuh.  The chunk's
 // rows share this work, which a fused kernel would repeat for every block of 64
-// of them (500 / 2048 tokens 147 / 250 us fused, 38 / 54 us with the workspace).
-// Bound by issue as a plain read is: 4096 tokens x 16 heads, residual, 18.5 us.
+// of them (500 / 2048 tokens 147 / 250 us fused, 48 / 70 us with the workspace).
+// Bound as a plain read is: 2048 tokens of 16 heads after the 1024 of their window
+// (residual, tail), 18.7 us, issue slots used in 62% of the cycles.
 #include "read.cuh"
 
 namespace rq {
